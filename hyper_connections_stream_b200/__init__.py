@@ -12,7 +12,9 @@ CUDA.
 from __future__ import annotations
 
 __all__ = ["sinkhorn", "read_rmsnorm", "write_mix", "write_then_read", "HCError",
-           "MIX_MATRIX", "MIX_SINKHORN_LOGITS", "READ_WEIGHTS", "READ_SOFTMAX_LOGITS"]
+           "MIX_MATRIX", "MIX_SINKHORN_LOGITS", "READ_WEIGHTS", "READ_SOFTMAX_LOGITS",
+           "Checkpoint", "checkpoint_pack", "checkpoint_unpack", "write_then_read_checkpoint",
+           "write_then_read_backward_checkpoint", "read_layernorm", "read_layernorm_backward"]
 
 
 def __getattr__(name):

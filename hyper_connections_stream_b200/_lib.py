@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -61,6 +62,21 @@ SIGNATURES = {
     "hc_ipc_export": ([_vp, _vp, C.POINTER(C.c_uint64)], _i32),
     "hc_ipc_open": ([_vp, C.POINTER(_vp)], _i32),
     "hc_ipc_close": ([_vp], _i32),
+    "hc_checkpoint_scale_stride": ([_i64], _i64),
+    "hc_checkpoint_pack": ([_vp, _i32, _i64, _i64, _vp, _vp, _vp], _i32),
+    "hc_checkpoint_unpack": ([_vp, _vp, _vp, _i32, _i64, _i64, _vp], _i32),
+    "hc_write_then_read_checkpoint": ([_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i64, _i32, _vp, _i64,
+                                       _i32, _vp, _i64, _i32, _vp, _i64, _vp, _f32, _vp, _vp, _vp,
+                                       _vp, _vp], _i32),
+    "hc_write_then_read_backward_checkpoint": ([_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i64, _i32, _vp,
+                                                _i64, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _f32, _vp,
+                                                _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, C.c_size_t,
+                                                _vp], _i32),
+    "hc_write_then_read_backward_checkpoint_workspace_bytes": ([_i32, _i64, _i32, _i64], C.c_size_t),
+    "hc_read_layernorm": ([_vp, _vp, _i32, _i64, _i32, _i64, _i32, _vp, _i64, _vp, _vp, _f32, _vp], _i32),
+    "hc_read_layernorm_backward": ([_vp, _vp, _i32, _i64, _i32, _i64, _i32, _vp, _i64, _vp, _f32, _vp,
+                                    _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp], _i32),
+    "hc_read_layernorm_backward_workspace_bytes": ([_i32, _i64, _i32, _i64], C.c_size_t),
     "hc_status_string": ([_i32], C.c_char_p),
     "hc_last_error": ([], C.c_char_p),
     "hc_version": ([], _i32),
@@ -587,4 +603,236 @@ def write_then_read_backward_noalloc(H, y, A, b, a, g, dHout, dx, *, eps: float 
         int(read), _ptr(a), a_s, _ptr(g), float(eps), _ptr(dHout), _ptr(dx), _ptr(out["dH"]),
         _ptr(out["dy"]), _ptr(out["dA"]), _ptr(out["db"]), _ptr(out["da"]), _ptr(out["dg"]),
         _stream(dev)))
+    return out
+
+
+class Checkpoint(NamedTuple):
+    """8-bit checkpoint of a tensor [..., d]: e4m3 codes [..., d] and, for
+    every block of 32 along d, the biased exponent of its power-of-two scale,
+    [..., checkpoint_scale_stride(d)] uint8."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def checkpoint_scale_stride(d: int) -> int:
+    """Scale bytes a row of d values takes: one per 32 values, padded to 16."""
+    return int(lib().hc_checkpoint_scale_stride(int(d)))
+
+
+def checkpoint_empty(shape, device) -> Checkpoint:
+    """Uninitialised checkpoint buffers for a tensor of this shape."""
+    return Checkpoint(torch.empty(tuple(shape), dtype=torch.float8_e4m3fn, device=device),
+                      torch.empty((*shape[:-1], checkpoint_scale_stride(shape[-1])), dtype=torch.uint8,
+                                  device=device))
+
+
+def _need_checkpoint(name, c, shape=None):
+    if not isinstance(c, Checkpoint):
+        raise TypeError(f"{name} must be a Checkpoint")
+    _need_cuda(f"{name}.codes", c.codes, torch.float8_e4m3fn)
+    if c.codes.dim() < 1:
+        raise ValueError(f"{name} must have a last dimension")
+    if shape is not None and tuple(c.codes.shape) != tuple(shape):
+        raise ValueError(f"{name} must be of shape {tuple(shape)}, got {tuple(c.codes.shape)}")
+    _need_out(f"{name}.scales", c.scales,
+              (*c.codes.shape[:-1], checkpoint_scale_stride(c.codes.shape[-1])), torch.uint8)
+
+
+def _rows(shape) -> int:
+    r = 1
+    for s in shape[:-1]:
+        r *= s
+    return r
+
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+
+
+def checkpoint_pack(x, *, out: Checkpoint | None = None) -> Checkpoint:
+    """8-bit checkpoint of x [..., d] (float32 or bfloat16): blocks of 32 along
+    d, each value e4m3 of x over the block's power of two. Values that are not
+    finite are kept as NaN."""
+    _need_cuda("x", x)
+    if x.dim() < 1 or x.dtype not in _DT:
+        raise ValueError("x must be [..., d] float32 or bfloat16")
+    out = checkpoint_empty(x.shape, x.device) if out is None else out
+    _need_checkpoint("out", out, x.shape)
+    _same_device(x, out=out.codes, out_scales=out.scales)
+    with torch.cuda.device(x.device):
+        _check(lib().hc_checkpoint_pack(_ptr(x), _DT[x.dtype], _rows(x.shape), x.shape[-1], _ptr(out.codes),
+                                        _ptr(out.scales), _stream(x.device)))
+    return out
+
+
+def checkpoint_unpack(c: Checkpoint, dtype=torch.bfloat16, *, out=None):
+    """The values a checkpoint keeps, [..., d] in dtype."""
+    _need_checkpoint("c", c)
+    if dtype not in _DT:
+        raise ValueError("dtype must be float32 or bfloat16")
+    shape = c.codes.shape
+    out = torch.empty(shape, dtype=dtype, device=c.codes.device) if out is None else out
+    _need_out("out", out, shape, dtype)
+    _same_device(c.codes, scales=c.scales, out=out)
+    with torch.cuda.device(out.device):
+        _check(lib().hc_checkpoint_unpack(_ptr(c.codes), _ptr(c.scales), _ptr(out), _DT[dtype], _rows(shape),
+                                          shape[-1], _stream(out.device)))
+    return out
+
+
+def write_then_read_checkpoint(H, y, A, b, a_next, g_next=None, *, eps: float = 1e-6,
+                               mix: int = MIX_MATRIX, K: int = 0, read: int = READ_WEIGHTS,
+                               out=None, x_next=None, H_ckpt: Checkpoint | None = None,
+                               y_ckpt: Checkpoint | None = None):
+    """write_then_read that also keeps an 8-bit checkpoint of its H and y (as
+    they are before the call: out may be H) for
+    write_then_read_backward_checkpoint. Returns (H', x_next, checkpoint of H,
+    checkpoint of y)."""
+    _need_cuda("H", H)
+    T, n, d = _streams_shape(H)
+    _need_cuda("y", y, H.dtype)
+    if tuple(y.shape) != (T, d):
+        raise ValueError("y must be [T, d]")
+    A_s = _tok_param("A", A, T, (n, n))
+    b_s = _tok_param("b", b, T, (n,))
+    a_s = _tok_param("a_next", a_next, T, (n,))
+    _need_gain("g_next", g_next, d)
+    out = torch.empty_like(H) if out is None else out
+    x_next = torch.empty((T, d), dtype=H.dtype, device=H.device) if x_next is None else x_next
+    _need_out("out", out, (T, n, d), H.dtype)
+    _need_out("x_next", x_next, (T, d), H.dtype)
+    H_ckpt = checkpoint_empty((T, n, d), H.device) if H_ckpt is None else H_ckpt
+    y_ckpt = checkpoint_empty((T, d), H.device) if y_ckpt is None else y_ckpt
+    _need_checkpoint("H_ckpt", H_ckpt, (T, n, d))
+    _need_checkpoint("y_ckpt", y_ckpt, (T, d))
+    _same_device(H, y=y, A=A, b=b, a_next=a_next, g_next=g_next, out=out, x_next=x_next, H_ckpt=H_ckpt.codes,
+                 H_ckpt_scales=H_ckpt.scales, y_ckpt=y_ckpt.codes, y_ckpt_scales=y_ckpt.scales)
+    with torch.cuda.device(H.device):
+        _check(lib().hc_write_then_read_checkpoint(
+            _ptr(H), _ptr(y), _ptr(out), _ptr(x_next), _DT[H.dtype], T, n, d, int(mix), _ptr(A), A_s, int(K),
+            _ptr(b), b_s, int(read), _ptr(a_next), a_s, _ptr(g_next), float(eps), _ptr(H_ckpt.codes),
+            _ptr(H_ckpt.scales), _ptr(y_ckpt.codes), _ptr(y_ckpt.scales), _stream(H.device)))
+    return out, x_next, H_ckpt, y_ckpt
+
+
+def write_then_read_backward_checkpoint(H_ckpt: Checkpoint, y_ckpt: Checkpoint, A, b, a, g, dHout, dx, *,
+                                        eps: float = 1e-6, mix: int = MIX_MATRIX, K: int = 0,
+                                        read: int = READ_WEIGHTS, want_dg: bool = True, workspace=None):
+    """Backward of write_then_read from the checkpoint of its H and y: the
+    gradients at the kept values (H' not rounded). dHout [T, n, d] (or None)
+    and dx [T, d] are the gradients arriving at H' and x_next; their dtype is
+    that of dH and dy. Returns the dict of write_then_read_backward."""
+    _need_cuda("dx", dx)
+    if dx.dim() != 2 or dx.dtype not in _DT:
+        raise ValueError("dx must be [T, d] float32 or bfloat16")
+    _need_checkpoint("H_ckpt", H_ckpt)
+    if H_ckpt.codes.dim() != 3:
+        raise ValueError("H_ckpt must be of shape [T, n, d]")
+    T, n, d = H_ckpt.codes.shape
+    _need_checkpoint("y_ckpt", y_ckpt, (T, d))
+    if tuple(dx.shape) != (T, d):
+        raise ValueError("dx must be [T, d]")
+    if dHout is not None:
+        _need_out("dHout", dHout, (T, n, d), dx.dtype)
+    A_s = _tok_param("A", A, T, (n, n))
+    b_s = _tok_param("b", b, T, (n,))
+    a_s = _tok_param("a", a, T, (n,))
+    _need_gain("g", g, d)
+    dev = dx.device
+    _same_device(dx, H_ckpt=H_ckpt.codes, H_ckpt_scales=H_ckpt.scales, y_ckpt=y_ckpt.codes,
+                 y_ckpt_scales=y_ckpt.scales, A=A, b=b, a=a, g=g, dHout=dHout, workspace=workspace)
+    out = dict(dH=torch.empty((T, n, d), dtype=dx.dtype, device=dev), dy=torch.empty_like(dx),
+               dA=torch.empty((T, n, n), dtype=torch.float32, device=dev),
+               db=torch.empty((T, n), dtype=torch.float32, device=dev),
+               da=torch.empty((T, n), dtype=torch.float32, device=dev),
+               dg=torch.empty((d,), dtype=torch.float32, device=dev) if (g is not None and want_dg)
+               else None)
+    with torch.cuda.device(dev):
+        ws_bytes = 0
+        if out["dg"] is not None:
+            if workspace is None:
+                need = int(lib().hc_write_then_read_backward_checkpoint_workspace_bytes(_DT[dx.dtype], T, n, d))
+                workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+            _need_cuda("workspace", workspace, torch.uint8)
+            ws_bytes = workspace.numel()
+        _check(lib().hc_write_then_read_backward_checkpoint(
+            _ptr(H_ckpt.codes), _ptr(H_ckpt.scales), _ptr(y_ckpt.codes), _ptr(y_ckpt.scales), _DT[dx.dtype],
+            T, n, d, int(mix), _ptr(A), A_s, int(K), _ptr(b), b_s, int(read), _ptr(a), a_s, _ptr(g), float(eps),
+            _ptr(dHout), _ptr(dx), _ptr(out["dH"]), _ptr(out["dy"]), _ptr(out["dA"]), _ptr(out["db"]),
+            _ptr(out["da"]), _ptr(out["dg"]), _ptr(workspace) if out["dg"] is not None else None, ws_bytes,
+            _stream(dev)))
+    return out
+
+
+def _read_param(a, T, n):
+    """Token stride of optional read weights (None: weight 1, one stream)."""
+    if a is None:
+        if n != 1:
+            raise ValueError("a may be None only for n = 1")
+        return 0
+    return _tok_param("a", a, T, (n,))
+
+
+def read_layernorm(H, a, g=None, beta=None, *, eps: float = 1e-6, read: int = READ_WEIGHTS, x=None):
+    """x = LayerNorm(sum_i a_i H_i) * g + beta. H [T, n, d]; a [n] or [T, n]
+    (weights or, with read=READ_SOFTMAX_LOGITS, logits), or None when n = 1
+    (the plain layer norm of T rows); g, beta [d] fp32 or None."""
+    _need_cuda("H", H)
+    T, n, d = _streams_shape(H)
+    a_s = _read_param(a, T, n)
+    _need_gain("g", g, d)
+    _need_gain("beta", beta, d)
+    x = torch.empty((T, d), dtype=H.dtype, device=H.device) if x is None else x
+    _need_out("x", x, (T, d), H.dtype)
+    _same_device(H, a=a, g=g, beta=beta, x=x)
+    with torch.cuda.device(H.device):
+        _check(lib().hc_read_layernorm(_ptr(H), _ptr(x), _DT[H.dtype], T, n, d, int(read), _ptr(a), a_s, _ptr(g),
+                                       _ptr(beta), float(eps), _stream(H.device)))
+    return x
+
+
+def read_layernorm_backward(H, a, g, dx, *, eps: float = 1e-6, read: int = READ_WEIGHTS,
+                            want_dg: bool = True, want_dbeta: bool = True, workspace=None):
+    """Backward of read_layernorm. H [T, n, d] (dtype of dx) or its Checkpoint
+    (the gradients are then those at the kept values); dx [T, d] the gradient
+    arriving at x. Returns a dict with dH [T, n, d], da [T, n] (fp32, per
+    token; w.r.t. the logits in the softmax mode; None without a), dg and
+    dbeta [d] (fp32, summed over tokens; dg is None without g). The workspace
+    is allocated here unless given."""
+    _need_cuda("dx", dx)
+    if dx.dim() != 2 or dx.dtype not in _DT:
+        raise ValueError("dx must be [T, d] float32 or bfloat16")
+    if isinstance(H, Checkpoint):
+        _need_checkpoint("H", H)
+        rows, scales = H.codes, H.scales
+    else:
+        _need_cuda("H", H, dx.dtype)
+        rows, scales = H, None
+    if rows.dim() != 3:
+        raise ValueError(f"H must be [T, n, d], got {tuple(rows.shape)}")
+    T, n, d = rows.shape
+    if tuple(dx.shape) != (T, d):
+        raise ValueError("dx must be [T, d]")
+    a_s = _read_param(a, T, n)
+    _need_gain("g", g, d)
+    dev = dx.device
+    _same_device(dx, H=rows, H_scales=scales, a=a, g=g, workspace=workspace)
+    f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)
+    out = dict(dH=torch.empty((T, n, d), dtype=dx.dtype, device=dev), da=f32(T, n) if a is not None else None,
+               dg=f32(d) if (g is not None and want_dg) else None, dbeta=f32(d) if want_dbeta else None)
+    with torch.cuda.device(dev):
+        ws_bytes = 0
+        sums = out["dg"] is not None or out["dbeta"] is not None
+        if sums:
+            if workspace is None:
+                need = int(lib().hc_read_layernorm_backward_workspace_bytes(_DT[dx.dtype], T, n, d))
+                workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+            _need_cuda("workspace", workspace, torch.uint8)
+            ws_bytes = workspace.numel()
+        _check(lib().hc_read_layernorm_backward(
+            _ptr(rows), _ptr(scales), _DT[dx.dtype], T, n, d, int(read), _ptr(a), a_s, _ptr(g), float(eps),
+            _ptr(dx), _ptr(out["dH"]), _ptr(out["da"]), _ptr(out["dg"]), _ptr(out["dbeta"]),
+            _ptr(workspace) if sums else None, ws_bytes, _stream(dev)))
     return out

@@ -17,6 +17,7 @@
 #include <atomic>
 
 #include "hc_api.h"
+#include "hc_checkpoint.cuh"
 #include "hc_launch.h"
 
 // The library's device fault word (one per device that loads the library).
@@ -145,6 +146,28 @@ hc_status check_K(const char *fn, int K) {
     return HC_OK;
 }
 
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+// Outputs must not overlap an input or one another (empty spans overlap nothing).
+template <int NI, int NO>
+hc_status check_disjoint(const char *fn, const Span (&ins)[NI], const Span (&outs)[NO]) {
+    for (int o = 0; o < NO; ++o) {
+        for (int i = 0; i < NI; ++i)
+            if (overlap(outs[o].p, outs[o].bytes, ins[i].p, ins[i].bytes))
+                return fail(HC_ERR_ALIAS, "%s: an output overlaps an input", fn);
+        for (int q = o + 1; q < NO; ++q)
+            if (overlap(outs[o].p, outs[o].bytes, outs[q].p, outs[q].bytes))
+                return fail(HC_ERR_ALIAS, "%s: two outputs overlap", fn);
+    }
+    return HC_OK;
+}
+
+// Bytes of T tokens' sets of a parameter: what the last token reaches.
+int64_t param_bytes(int64_t T, int64_t stride, int64_t per) { return 4 * ((T - 1) * stride + per); }
+
 #define HC_TRY(expr)                       \
     do {                                   \
         hc_status _st = (expr);            \
@@ -165,7 +188,7 @@ hc_status dispatch(hc_dtype dt, int n, const hc::StepParams &p, cudaStream_t st)
 
 extern "C" {
 
-int hc_version(void) { return 300; }
+int hc_version(void) { return 400; }
 
 const char *hc_status_string(hc_status st) {
     switch (st) {
@@ -768,6 +791,294 @@ hc_status hc_write_then_read_backward(const void *H, const void *y, hc_dtype dt,
     ba.dA = dA; ba.db = db; ba.da = da; ba.dg = dg;
     ba.workspace = workspace; ba.workspace_bytes = workspace_bytes;
     return hc::launch_backward(ba, ctx, static_cast<cudaStream_t>(stream));
+}
+
+int64_t hc_checkpoint_scale_stride(int64_t d) { return d < 1 ? 0 : hc::ck_scale_stride(d); }
+
+hc_status hc_checkpoint_pack(const void *X, hc_dtype dt, int64_t rows, int64_t d, uint8_t *codes,
+                             uint8_t *scales, hc_stream stream) {
+    static const char *fn = "hc_checkpoint_pack";
+    g_last_error[0] = '\0';
+    HC_TRY(check_shape(fn, Shape{dt, rows, 1, d}, false));
+    if (d > (int64_t(1) << 30)) return fail(HC_ERR_UNSUPPORTED, "%s: d > 2^30", fn);
+    if (rows == 0) return HC_OK;
+    HC_TRY(check_buf(fn, "X", X));
+    HC_TRY(check_buf(fn, "codes", codes));
+    HC_TRY(check_buf(fn, "scales", scales));
+    const Span ins[] = {{X, rows * d * elem_bytes(dt)}};
+    const Span outs[] = {{codes, rows * d}, {scales, rows * hc::ck_scale_stride(d)}};
+    HC_TRY(check_disjoint(fn, ins, outs));
+    hc::LaunchCtx ctx{};
+    HC_TRY(launch_ctx(ctx));
+    return hc::launch_checkpoint_pack(X, dt, codes, scales, rows, d, ctx, static_cast<cudaStream_t>(stream));
+}
+
+hc_status hc_checkpoint_unpack(const uint8_t *codes, const uint8_t *scales, void *X, hc_dtype dt, int64_t rows,
+                               int64_t d, hc_stream stream) {
+    static const char *fn = "hc_checkpoint_unpack";
+    g_last_error[0] = '\0';
+    HC_TRY(check_shape(fn, Shape{dt, rows, 1, d}, false));
+    if (d > (int64_t(1) << 30)) return fail(HC_ERR_UNSUPPORTED, "%s: d > 2^30", fn);
+    if (rows == 0) return HC_OK;
+    HC_TRY(check_buf(fn, "codes", codes));
+    HC_TRY(check_buf(fn, "scales", scales));
+    HC_TRY(check_buf(fn, "X", X));
+    const Span ins[] = {{codes, rows * d}, {scales, rows * hc::ck_scale_stride(d)}};
+    const Span outs[] = {{X, rows * d * elem_bytes(dt)}};
+    HC_TRY(check_disjoint(fn, ins, outs));
+    hc::LaunchCtx ctx{};
+    HC_TRY(launch_ctx(ctx));
+    return hc::launch_checkpoint_unpack(codes, scales, X, dt, rows, d, ctx, static_cast<cudaStream_t>(stream));
+}
+
+hc_status hc_write_then_read_checkpoint(const void *H, const void *y, void *Hout, void *x_next, hc_dtype dt,
+                                        int64_t T, int n, int64_t d, hc_mix_mode mm, const float *A,
+                                        int64_t A_tok_stride, int K, const float *b, int64_t b_tok_stride,
+                                        hc_read_mode rm, const float *a_next, int64_t a_tok_stride,
+                                        const float *g_next, float eps, uint8_t *H_codes, uint8_t *H_scales,
+                                        uint8_t *y_codes, uint8_t *y_scales, hc_stream stream) {
+    static const char *fn = "hc_write_then_read_checkpoint";
+    g_last_error[0] = '\0';
+    const Shape s{dt, T, n, d};
+    HC_TRY(check_shape(fn, s, true));
+    if (mm != HC_MIX_MATRIX && mm != HC_MIX_SINKHORN_LOGITS)
+        return fail(HC_ERR_INVALID_ARG, "%s: bad mix mode %d", fn, (int)mm);
+    if (rm != HC_READ_WEIGHTS && rm != HC_READ_SOFTMAX_LOGITS)
+        return fail(HC_ERR_INVALID_ARG, "%s: bad read mode %d", fn, (int)rm);
+    if (mm == HC_MIX_SINKHORN_LOGITS) HC_TRY(check_K(fn, K));
+    HC_TRY(check_stride(fn, "A_tok_stride", A_tok_stride));
+    HC_TRY(check_stride(fn, "b_tok_stride", b_tok_stride));
+    HC_TRY(check_stride(fn, "a_tok_stride", a_tok_stride));
+    HC_TRY(check_eps(fn, eps));
+    if (T == 0) return HC_OK;
+    HC_TRY(check_buf(fn, "H", H));
+    HC_TRY(check_buf(fn, "y", y));
+    HC_TRY(check_buf(fn, "Hout", Hout));
+    HC_TRY(check_buf(fn, "x_next", x_next));
+    HC_TRY(check_buf(fn, "H_codes", H_codes));
+    HC_TRY(check_buf(fn, "H_scales", H_scales));
+    HC_TRY(check_buf(fn, "y_codes", y_codes));
+    HC_TRY(check_buf(fn, "y_scales", y_scales));
+    HC_TRY(check_param(fn, "A", A));
+    HC_TRY(check_param(fn, "b", b));
+    HC_TRY(check_param(fn, "a_next", a_next));
+    if (g_next && !aligned(g_next, 16))
+        return fail(HC_ERR_MISALIGNED, "%s: g_next is not 16-byte aligned", fn);
+    const int64_t es = elem_bytes(dt), ns = hc::ck_scale_stride(d);
+    const int64_t hb = T * n * d * es, yb = T * d * es;
+    const Span ins[] = {{Hout == H ? nullptr : H, hb},
+                        {y, yb},
+                        {A, param_bytes(T, A_tok_stride, n * n)},
+                        {b, param_bytes(T, b_tok_stride, n)},
+                        {a_next, param_bytes(T, a_tok_stride, n)},
+                        {g_next, d * 4}};
+    const Span outs[] = {{Hout, hb},       {x_next, yb},          {H_codes, T * n * d},
+                         {H_scales, T * n * ns}, {y_codes, T * d}, {y_scales, T * ns}};
+    HC_TRY(check_disjoint(fn, ins, outs));
+    hc::StepParams p{};
+    p.H = H; p.y = y; p.Hout = Hout; p.x = x_next; p.T = T; p.d = d;
+    p.A = A; p.A_s = A_tok_stride; p.b = b; p.b_s = b_tok_stride;
+    p.a = a_next; p.a_s = a_tok_stride; p.g = g_next; p.eps = eps;
+    p.K = K; p.mix_logits = mm == HC_MIX_SINKHORN_LOGITS;
+    p.read_logits = rm == HC_READ_SOFTMAX_LOGITS;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    hc::LaunchCtx ctx{};
+    HC_TRY(launch_ctx(ctx));
+    HC_TRY(hc::launch_checkpoint_pack(H, dt, H_codes, H_scales, T * n, d, ctx, st));
+    HC_TRY(hc::launch_checkpoint_pack(y, dt, y_codes, y_scales, T, d, ctx, st));
+    return dispatch<hc::KIND_FUSED>(dt, n, p, st);
+}
+
+size_t hc_write_then_read_backward_checkpoint_workspace_bytes(hc_dtype dt, int64_t T, int n, int64_t d) {
+    if ((dt != HC_F32 && dt != HC_BF16) || T < 1 || n < 1 || n > hc::kMaxStreams || d < 1) return 0;
+    hc::LaunchCtx ctx{};
+    if (launch_ctx(ctx) != HC_OK) return 0;
+    size_t bytes = 0;
+    if (hc::checkpoint_backward_workspace_bytes(n, dt, T, d, ctx, &bytes) != HC_OK) return 0;
+    return bytes;
+}
+
+hc_status hc_write_then_read_backward_checkpoint(
+    const uint8_t *H_codes, const uint8_t *H_scales, const uint8_t *y_codes, const uint8_t *y_scales, hc_dtype dt,
+    int64_t T, int n, int64_t d, hc_mix_mode mm, const float *A, int64_t A_tok_stride, int K, const float *b,
+    int64_t b_tok_stride, hc_read_mode rm, const float *a, int64_t a_tok_stride, const float *g, float eps,
+    const void *dHout, const void *dx, void *dH, void *dy, float *dA, float *db, float *da, float *dg,
+    void *workspace, size_t workspace_bytes, hc_stream stream) {
+    static const char *fn = "hc_write_then_read_backward_checkpoint";
+    g_last_error[0] = '\0';
+    const Shape s{dt, T, n, d};
+    HC_TRY(check_shape(fn, s, true));
+    if (mm != HC_MIX_MATRIX && mm != HC_MIX_SINKHORN_LOGITS)
+        return fail(HC_ERR_INVALID_ARG, "%s: bad mix mode %d", fn, (int)mm);
+    if (rm != HC_READ_WEIGHTS && rm != HC_READ_SOFTMAX_LOGITS)
+        return fail(HC_ERR_INVALID_ARG, "%s: bad read mode %d", fn, (int)rm);
+    if (mm == HC_MIX_SINKHORN_LOGITS) HC_TRY(check_K(fn, K));
+    HC_TRY(check_stride(fn, "A_tok_stride", A_tok_stride));
+    HC_TRY(check_stride(fn, "b_tok_stride", b_tok_stride));
+    HC_TRY(check_stride(fn, "a_tok_stride", a_tok_stride));
+    HC_TRY(check_eps(fn, eps));
+    if (T == 0) {  // nothing to sum: the gain's gradient is zero
+        if (dg && aligned(dg, 4)) {
+            const cudaError_t e = cudaMemsetAsync(dg, 0, (size_t)d * 4, static_cast<cudaStream_t>(stream));
+            if (e != cudaSuccess) return fail(HC_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+        }
+        return HC_OK;
+    }
+    HC_TRY(check_buf(fn, "H_codes", H_codes));
+    HC_TRY(check_buf(fn, "H_scales", H_scales));
+    HC_TRY(check_buf(fn, "y_codes", y_codes));
+    HC_TRY(check_buf(fn, "y_scales", y_scales));
+    HC_TRY(check_buf(fn, "dx", dx));
+    HC_TRY(check_buf(fn, "dH", dH));
+    HC_TRY(check_buf(fn, "dy", dy));
+    if (dHout && !aligned(dHout, 16)) return fail(HC_ERR_MISALIGNED, "%s: dHout is not 16-byte aligned", fn);
+    HC_TRY(check_param(fn, "A", A));
+    HC_TRY(check_param(fn, "b", b));
+    HC_TRY(check_param(fn, "a", a));
+    HC_TRY(check_param(fn, "dA", dA));
+    HC_TRY(check_param(fn, "db", db));
+    HC_TRY(check_param(fn, "da", da));
+    if (g && !aligned(g, 16)) return fail(HC_ERR_MISALIGNED, "%s: g is not 16-byte aligned", fn);
+    if (dg) {
+        if (!g) return fail(HC_ERR_INVALID_ARG, "%s: dg requested without a gain g", fn);
+        if (!aligned(dg, 4)) return fail(HC_ERR_MISALIGNED, "%s: dg is not 4-byte aligned", fn);
+        if (!workspace) return fail(HC_ERR_INVALID_ARG, "%s: dg needs a workspace", fn);
+        if (!aligned(workspace, 16)) return fail(HC_ERR_MISALIGNED, "%s: workspace is not 16-byte aligned", fn);
+    }
+    const int64_t es = elem_bytes(dt), ns = hc::ck_scale_stride(d);
+    const int64_t hb = T * n * d * es, yb = T * d * es;
+    const Span ins[] = {{H_codes, T * n * d},
+                        {H_scales, T * n * ns},
+                        {y_codes, T * d},
+                        {y_scales, T * ns},
+                        {dx, yb},
+                        {dHout, hb},
+                        {A, param_bytes(T, A_tok_stride, n * n)},
+                        {b, param_bytes(T, b_tok_stride, n)},
+                        {a, param_bytes(T, a_tok_stride, n)},
+                        {g, d * 4}};
+    const Span outs[] = {{dH, hb},         {dy, yb},         {dA, T * n * n * 4},
+                         {db, T * n * 4},  {da, T * n * 4},  {dg, dg ? d * 4 : 0},
+                         {workspace, dg ? (int64_t)workspace_bytes : 0}};
+    HC_TRY(check_disjoint(fn, ins, outs));
+    hc::LaunchCtx ctx{};
+    HC_TRY(launch_ctx(ctx));
+    hc::BackwardArgs ba{};
+    ba.f.H = H_codes; ba.f.y = y_codes; ba.f.T = T; ba.f.d = d;
+    ba.f.A = A; ba.f.A_s = A_tok_stride; ba.f.b = b; ba.f.b_s = b_tok_stride;
+    ba.f.a = a; ba.f.a_s = a_tok_stride; ba.f.g = g; ba.f.eps = eps;
+    ba.f.K = K; ba.f.mix_logits = mm == HC_MIX_SINKHORN_LOGITS;
+    ba.f.read_logits = rm == HC_READ_SOFTMAX_LOGITS;
+    ba.n = n; ba.dt = dt;
+    ba.dHout = dHout; ba.dx = dx; ba.dH = dH; ba.dy = dy;
+    ba.dA = dA; ba.db = db; ba.da = da; ba.dg = dg;
+    ba.workspace = workspace; ba.workspace_bytes = workspace_bytes;
+    return hc::launch_checkpoint_backward(ba, H_scales, y_scales, ctx, static_cast<cudaStream_t>(stream));
+}
+
+hc_status hc_read_layernorm(const void *H, void *x, hc_dtype dt, int64_t T, int n, int64_t d, hc_read_mode rm,
+                            const float *a, int64_t a_tok_stride, const float *g, const float *beta, float eps,
+                            hc_stream stream) {
+    static const char *fn = "hc_read_layernorm";
+    g_last_error[0] = '\0';
+    HC_TRY(check_shape(fn, Shape{dt, T, n, d}, true));
+    if (rm != HC_READ_WEIGHTS && rm != HC_READ_SOFTMAX_LOGITS)
+        return fail(HC_ERR_INVALID_ARG, "%s: bad read mode %d", fn, (int)rm);
+    HC_TRY(check_stride(fn, "a_tok_stride", a_tok_stride));
+    HC_TRY(check_eps(fn, eps));
+    if (T == 0) return HC_OK;
+    HC_TRY(check_buf(fn, "H", H));
+    HC_TRY(check_buf(fn, "x", x));
+    if (a || n > 1) HC_TRY(check_param(fn, "a", a));
+    if (g && !aligned(g, 16)) return fail(HC_ERR_MISALIGNED, "%s: g is not 16-byte aligned", fn);
+    if (beta && !aligned(beta, 16)) return fail(HC_ERR_MISALIGNED, "%s: beta is not 16-byte aligned", fn);
+    const int64_t es = elem_bytes(dt);
+    const Span ins[] = {{H, T * n * d * es},
+                        {a, a ? param_bytes(T, a_tok_stride, n) : 0},
+                        {g, d * 4},
+                        {beta, d * 4}};
+    const Span outs[] = {{x, T * d * es}};
+    HC_TRY(check_disjoint(fn, ins, outs));
+    hc::LaunchCtx ctx{};
+    HC_TRY(launch_ctx(ctx));
+    hc::LayerNormArgs la{};
+    la.f.H = H; la.f.x = x; la.f.T = T; la.f.d = d;
+    la.f.a = a; la.f.a_s = a_tok_stride; la.f.g = g; la.f.eps = eps;
+    la.f.read_logits = rm == HC_READ_SOFTMAX_LOGITS;
+    la.beta = beta;
+    la.n = n; la.dt = dt;
+    return hc::launch_layernorm(la, ctx, static_cast<cudaStream_t>(stream));
+}
+
+size_t hc_read_layernorm_backward_workspace_bytes(hc_dtype dt, int64_t T, int n, int64_t d) {
+    if ((dt != HC_F32 && dt != HC_BF16) || T < 1 || n < 1 || n > hc::kMaxStreams || d < 1) return 0;
+    hc::LaunchCtx ctx{};
+    if (launch_ctx(ctx) != HC_OK) return 0;
+    size_t bytes = 0;
+    if (hc::layernorm_backward_workspace_bytes(n, dt, T, d, ctx, &bytes) != HC_OK) return 0;
+    return bytes;
+}
+
+hc_status hc_read_layernorm_backward(const void *H, const uint8_t *H_scales, hc_dtype dt, int64_t T, int n,
+                                     int64_t d, hc_read_mode rm, const float *a, int64_t a_tok_stride,
+                                     const float *g, float eps, const void *dx, void *dH, float *da, float *dg,
+                                     float *dbeta, void *workspace, size_t workspace_bytes, hc_stream stream) {
+    static const char *fn = "hc_read_layernorm_backward";
+    g_last_error[0] = '\0';
+    HC_TRY(check_shape(fn, Shape{dt, T, n, d}, true));
+    if (rm != HC_READ_WEIGHTS && rm != HC_READ_SOFTMAX_LOGITS)
+        return fail(HC_ERR_INVALID_ARG, "%s: bad read mode %d", fn, (int)rm);
+    HC_TRY(check_stride(fn, "a_tok_stride", a_tok_stride));
+    HC_TRY(check_eps(fn, eps));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {  // nothing to sum: the gradients of g and beta are zero
+        for (float *o : {dg, dbeta}) {
+            if (!o || !aligned(o, 4)) continue;
+            const cudaError_t e = cudaMemsetAsync(o, 0, (size_t)d * 4, st);
+            if (e != cudaSuccess) return fail(HC_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+        }
+        return HC_OK;
+    }
+    HC_TRY(check_buf(fn, "H", H));
+    if (H_scales && !aligned(H_scales, 16))
+        return fail(HC_ERR_MISALIGNED, "%s: H_scales is not 16-byte aligned", fn);
+    HC_TRY(check_buf(fn, "dx", dx));
+    HC_TRY(check_buf(fn, "dH", dH));
+    if (a || n > 1) HC_TRY(check_param(fn, "a", a));
+    if (da && !a) return fail(HC_ERR_INVALID_ARG, "%s: da requested without weights a", fn);
+    if (da && !aligned(da, 4)) return fail(HC_ERR_MISALIGNED, "%s: da is not 4-byte aligned", fn);
+    if (g && !aligned(g, 16)) return fail(HC_ERR_MISALIGNED, "%s: g is not 16-byte aligned", fn);
+    const bool want = dg || dbeta;
+    if (want) {
+        if (dg && !g) return fail(HC_ERR_INVALID_ARG, "%s: dg requested without a gain g", fn);
+        if ((dg && !aligned(dg, 4)) || (dbeta && !aligned(dbeta, 4)))
+            return fail(HC_ERR_MISALIGNED, "%s: dg or dbeta is not 4-byte aligned", fn);
+        if (!workspace) return fail(HC_ERR_INVALID_ARG, "%s: dg and dbeta need a workspace", fn);
+        if (!aligned(workspace, 16)) return fail(HC_ERR_MISALIGNED, "%s: workspace is not 16-byte aligned", fn);
+    }
+    const int64_t es = elem_bytes(dt);
+    const Span ins[] = {{H, T * n * d * (H_scales ? 1 : es)},
+                        {H_scales, H_scales ? T * n * hc::ck_scale_stride(d) : 0},
+                        {dx, T * d * es},
+                        {a, a ? param_bytes(T, a_tok_stride, n) : 0},
+                        {g, d * 4}};
+    const Span outs[] = {{dH, T * n * d * es},
+                         {da, da ? T * n * 4 : 0},
+                         {dg, dg ? d * 4 : 0},
+                         {dbeta, dbeta ? d * 4 : 0},
+                         {workspace, want ? (int64_t)workspace_bytes : 0}};
+    HC_TRY(check_disjoint(fn, ins, outs));
+    hc::LaunchCtx ctx{};
+    HC_TRY(launch_ctx(ctx));
+    hc::LayerNormArgs la{};
+    la.f.H = H; la.f.T = T; la.f.d = d;
+    la.f.a = a; la.f.a_s = a_tok_stride; la.f.g = g; la.f.eps = eps;
+    la.f.read_logits = rm == HC_READ_SOFTMAX_LOGITS;
+    la.n = n; la.dt = dt;
+    la.sH = H_scales;
+    la.dx = dx; la.dH = dH; la.da = da; la.dg = dg; la.dbeta = dbeta;
+    la.workspace = workspace; la.workspace_bytes = workspace_bytes;
+    return hc::launch_layernorm_backward(la, ctx, st);
 }
 
 }  // extern "C"

@@ -657,17 +657,33 @@ struct StepBw {
         if (grid < 1) grid = 1;
         return HC_OK;
     }
-    static hc_status launch(const BackwardArgs &a, const LaunchCtx &ctx, cudaStream_t st) {
-        // the Sinkhorn backward's iterates must fit shared memory: check before any launch
-        int pthreads = 128;
+    // Threads and shared memory of the parameter backward: the Sinkhorn
+    // backward's iterates must fit (checked before any launch).
+    static hc_status param_shape(const BackwardArgs &a, size_t &hist, int &pthreads) {
+        pthreads = 128;
         const int Kh = a.f.mix_logits ? a.f.K : 0;
-        size_t hist = (size_t)(2 * Kh + 1) * pthreads * Group<N>::EPL * 4;
+        hist = (size_t)(2 * Kh + 1) * pthreads * Group<N>::EPL * 4;
         if (hist > (size_t)kSmemLimitLogits - 4096) {
             pthreads = 32;
             hist = (size_t)(2 * Kh + 1) * pthreads * Group<N>::EPL * 4;
         }
         if (hist > (size_t)kSmemLimitLogits - 4096)
             return set_error(HC_ERR_UNSUPPORTED, "K = %d too large for the Sinkhorn backward", a.f.K);
+        return HC_OK;
+    }
+    // The parameter backward and the gain reduction alone, over `rows` partial
+    // rows of the workspace (st unused when only checking).
+    static hc_status tail(const BackwardArgs &a, int64_t rows, bool check_only, const LaunchCtx &ctx,
+                          cudaStream_t st) {
+        int pthreads = 0;
+        size_t hist = 0;
+        HC_BW_TRY(param_shape(a, hist, pthreads));
+        return check_only ? HC_OK : launch_tail(a, ctx, st, rows, hist, pthreads);
+    }
+    static hc_status launch(const BackwardArgs &a, const LaunchCtx &ctx, cudaStream_t st) {
+        int pthreads = 0;
+        size_t hist = 0;
+        HC_BW_TRY(param_shape(a, hist, pthreads));
         const bool want_dg = a.dg != nullptr;
         int NT = 0;
         int64_t grid = 0;
@@ -785,7 +801,30 @@ hc_status dispatch_bw(const BackwardArgs &a, const LaunchCtx &ctx, cudaStream_t 
     }
 }
 
+// The parameter kernels work on fp32 per-token sums whatever the streams' type.
+hc_status dispatch_bw_tail(const BackwardArgs &a, int64_t rows, bool check_only, const LaunchCtx &ctx,
+                           cudaStream_t st) {
+    switch (a.n) {
+        case 1: return StepBw<1, float>::tail(a, rows, check_only, ctx, st);
+        case 2: return StepBw<2, float>::tail(a, rows, check_only, ctx, st);
+        case 3: return StepBw<3, float>::tail(a, rows, check_only, ctx, st);
+        case 4: return StepBw<4, float>::tail(a, rows, check_only, ctx, st);
+        case 5: return StepBw<5, float>::tail(a, rows, check_only, ctx, st);
+        case 6: return StepBw<6, float>::tail(a, rows, check_only, ctx, st);
+        case 7: return StepBw<7, float>::tail(a, rows, check_only, ctx, st);
+        default: return StepBw<8, float>::tail(a, rows, check_only, ctx, st);
+    }
+}
+
 }  // namespace
+
+hc_status check_param_backward(const BackwardArgs &a) {
+    return dispatch_bw_tail(a, 0, true, LaunchCtx{}, nullptr);
+}
+
+hc_status launch_backward_tail(const BackwardArgs &a, int64_t rows, const LaunchCtx &ctx, cudaStream_t st) {
+    return dispatch_bw_tail(a, rows, false, ctx, st);
+}
 
 hc_status backward_workspace_bytes(int n, hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx,
                                    size_t *bytes) {

@@ -1,0 +1,385 @@
+// hc_checkpoint_backward.cu -- backward of the fused HC step from the 8-bit
+// checkpoint of its H and y.
+//
+// The gradients of  H'_j = sum_i A_ij H_i + b_j y,  h = sum_j a_j H'_j,
+// x = h r g,  r = (mean h^2 + eps)^(-1/2)  at the checkpoint's values, H' not
+// rounded. With H' linear in H and y so is h, and everything that multiplies
+// them can be summed before the token's statistic is known:
+//   h    = sum_i c_i H_i + c_y y,      c_i = sum_j A_ij a_j, c_y = sum_j a_j b_j
+//   u    = g dx,   dh = r u - q h,     q = (r^3 / d) sum u h
+//   P_i  = <dh, H_i> = r <u, H_i> - q <h, H_i>,   P_y likewise with y
+//   dA_ij = <H_i, dH'_j> + a_j P_i     db_j = <y, dH'_j> + a_j P_y
+//   da_j  = sum_i A_ij P_i + b_j P_y   dg = sum_t dx h r
+//   dH_i = sum_j A_ij dH'_j + c_i dh   dy = sum_j b_j dH'_j + c_y dh
+// So the first pass over a token takes n^2 + 3n + 4 sums and the checkpoint is
+// read there only; the second needs dH', dx and h. Against taking the sums
+// after dh is known (H and y read and decoded twice, n^2 + n products each to
+// rebuild H') this leaves about half the arithmetic.
+//
+// hc_ck_bwd_kernel: a CTA takes a token at a time; threads own 16-byte column
+// slices. dH' and dx are read again from L2 in the second pass, h is parked in
+// shared memory (fp32; rebuilt from the checkpoint where a row does not fit).
+// The gain gradient accumulates in the CTA's workspace row.
+#include "hc_checkpoint.cuh"
+#include "hc_launch.h"
+#include "hc_token_sums.cuh"
+
+namespace hc {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTB = 32;  // parameter slots per batch
+
+struct CkBwParams {
+    StepParams f;          // H and y hold the codes
+    const uint8_t *sH, *sy;
+    int64_t ns;            // exponent bytes per row
+    const void *dHout, *dx;
+    void *dH, *dy;
+    float *gA, *gb, *ga;   // per-token sums (w.r.t. the matrix and the weights)
+    float *dg_part;        // [gridDim.x][d] or null
+};
+
+// Sums of a token, in this order: dA [n][n], db [n], <u, H_i> and <u, y>
+// [n + 1], <h, H_i> and <h, y> [n + 1], sum h^2, sum u h.
+template <int N> struct CkSums {
+    static constexpr int B = N * N, U = B + N, H = U + N + 1, SS = H + N + 1, SG = SS + 1, COUNT = SG + 1;
+};
+
+// From the warps' partial sums (red [warps][COUNT]) to r and q in stat[0 .. 1];
+// called by one warp, which then writes the token's parameter gradients with
+// ck_write_params.
+template <int N>
+__device__ __forceinline__ void ck_finish_sums(const float *red, int nwarps, double *fin, float *stat, int64_t d,
+                                               float eps, int lane) {
+    using Q = CkSums<N>;
+    for (int v = lane; v < Q::COUNT; v += 32) {
+        double s = 0.0;
+        for (int w = 0; w < nwarps; ++w) s += (double)red[w * Q::COUNT + v];
+        fin[v] = s;
+    }
+    __syncwarp();
+    if (lane == 0) {
+        const float r = __double2float_rn(1.0 / sqrt(fin[Q::SS] / (double)d + (double)eps));
+        const double rd = (double)r;
+        stat[0] = r;
+        stat[1] = (float)(rd * rd * rd * fin[Q::SG] / (double)d);
+    }
+    __syncwarp();
+}
+
+template <int N>
+__device__ __forceinline__ void ck_write_params(const double *fin, const float *stat, const float *At,
+                                                const float *bt, const float *at, float *gA, float *gb, float *ga,
+                                                int64_t t, int lane) {
+    using Q = CkSums<N>;
+    const double r = (double)stat[0], q = (double)stat[1];
+    for (int e = lane; e < N * N; e += 32) {
+        const int i = e / N, j = e - i * N;
+        gA[t * (N * N) + e] = (float)(fin[e] + (double)at[j] * (r * fin[Q::U + i] - q * fin[Q::H + i]));
+    }
+    if (lane < N) {
+        const double py = r * fin[Q::U + N] - q * fin[Q::H + N];
+        gb[t * N + lane] = (float)(fin[Q::B + lane] + (double)at[lane] * py);
+        double s = (double)bt[lane] * py;
+#pragma unroll
+        for (int i = 0; i < N; ++i) s += (double)At[i * N + lane] * (r * fin[Q::U + i] - q * fin[Q::H + i]);
+        ga[t * N + lane] = (float)s;
+    }
+    __syncwarp();
+}
+
+template <int N, typename S, bool PARK>
+__global__ void __launch_bounds__(kThreads, (N <= 4 ? 2 : 1))
+hc_ck_bwd_kernel(CkBwParams bp) {
+    const StepParams &p = bp.f;
+    constexpr int V = StorageTraits<S>::V, VP = V / 2, NN = N * N;
+    using Q = CkSums<N>;
+    constexpr int NV = Q::COUNT, NW = kThreads / 32;
+    __shared__ float sA[kTB * NN], sb[kTB * N], sa[kTB * N], sc[kTB * (N + 1)];
+    __shared__ float red[NW * NV];
+    __shared__ double fin[NV];
+    __shared__ float stat[2];
+    __shared__ float swork[NW * kGroupScratch];
+    extern __shared__ __align__(16) float shp[];  // [d] parked h
+
+    const int tid = threadIdx.x, NT = blockDim.x, nwarps = NT >> 5;
+    const int lane = tid & 31, warp = tid >> 5;
+    const int64_t d = p.d, nvec = d / V, G = gridDim.x;
+    int TB = nwarps * Group<N>::TPW;
+    TB = TB < kTB ? TB : kTB;
+    const uint8_t *QH = static_cast<const uint8_t *>(p.H), *QY = static_cast<const uint8_t *>(p.y);
+    const S *DX = static_cast<const S *>(bp.dx), *DHO = static_cast<const S *>(bp.dHout);
+    S *DH = static_cast<S *>(bp.dH), *DY = static_cast<S *>(bp.dy);
+    float *sdg = bp.dg_part ? bp.dg_part + (int64_t)blockIdx.x * d : nullptr;
+    if (sdg)
+        for (int64_t c = tid; c < nvec; c += NT) {
+#pragma unroll
+            for (int e = 0; e < V; e += 4)
+                *reinterpret_cast<float4 *>(sdg + c * V + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+
+    for (int64_t m0 = 0;; m0 += TB) {
+        const int64_t first = blockIdx.x + m0 * G;
+        if (first >= p.T) break;
+        __syncthreads();  // previous batch's parameters no longer read
+        prepare_params<N, true, true>(p, first, G, TB, sA, sb, sa, swork);
+        __syncthreads();
+        for (int v = tid; v < TB * (N + 1); v += NT) {
+            const int tt = v / (N + 1), i = v - tt * (N + 1);
+            if (first + (int64_t)tt * G >= p.T) continue;
+            float c = 0.0f;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                c = __fmaf_rn(i < N ? sA[tt * NN + i * N + j] : sb[tt * N + j], sa[tt * N + j], c);
+            sc[v] = c;
+        }
+        __syncthreads();
+        for (int tt = 0; tt < TB; ++tt) {
+            const int64_t t = first + (int64_t)tt * G;
+            if (t >= p.T) break;  // uniform over the CTA
+            const float *At = sA + tt * NN, *bt = sb + tt * N, *at = sa + tt * N, *ct = sc + tt * (N + 1);
+
+            // the checkpoint's values of slice k: H rows, then y
+            auto load_kept = [&](int64_t k, float2 (&hv)[N + 1][VP]) {
+#pragma unroll
+                for (int i = 0; i <= N; ++i) {
+                    const int64_t row = i < N ? t * N + i : t;
+                    uint32_t q[V / 4];
+                    ck_load<V>((i < N ? QH : QY) + row * d + k, q);
+                    const uint32_t e = __ldg((i < N ? bp.sH : bp.sy) + row * bp.ns + k / kCkBlock);
+                    ck_decode<VP>(q, ck_scale(e), hv[i]);
+                }
+            };
+            auto mix_h = [&](const float2 (&hv)[N + 1][VP], float2 (&h)[VP]) {
+#pragma unroll
+                for (int e = 0; e < VP; ++e) h[e] = fmul2_rn(make_float2(ct[0], ct[0]), hv[0][e]);
+#pragma unroll
+                for (int i = 1; i <= N; ++i)
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) h[e] = ffma2_rn(make_float2(ct[i], ct[i]), hv[i][e], h[e]);
+            };
+
+            // ---- pass 1: the token's sums ----
+            float acc[NV];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) acc[v] = 0.0f;
+            for (int64_t c = tid; c < nvec; c += NT) {
+                const int64_t k = c * V;
+                float2 hv[N + 1][VP], h[VP], u[VP], gv[VP];
+                load_kept(k, hv);
+                ck_widen(__ldg(reinterpret_cast<const uint4 *>(DX + t * d + k)), u);
+                load_gain2<VP>(p.g, k, gv);
+#pragma unroll
+                for (int e = 0; e < VP; ++e) u[e] = fmul2_rn(u[e], gv[e]);
+                mix_h(hv, h);
+                if constexpr (PARK) {
+#pragma unroll
+                    for (int e = 0; e < VP; e += 2)
+                        *reinterpret_cast<float4 *>(shp + k + 2 * e) =
+                            make_float4(h[e].x, h[e].y, h[e + 1].x, h[e + 1].y);
+                }
+                // a slice's product is summed in pairs, then added to the thread's sum
+                auto dot = [&](const float2 (&x)[VP], const float2 (&y)[VP], float &s) {
+                    float2 z = fmul2_rn(x[0], y[0]);
+#pragma unroll
+                    for (int e = 1; e < VP; ++e) z = ffma2_rn(x[e], y[e], z);
+                    s += z.x + z.y;
+                };
+#pragma unroll
+                for (int i = 0; i <= N; ++i) {
+                    dot(u, hv[i], acc[Q::U + i]);
+                    dot(h, hv[i], acc[Q::H + i]);
+                }
+                dot(h, h, acc[Q::SS]);
+                dot(u, h, acc[Q::SG]);
+                if (DHO) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        float2 gr[VP];
+                        ck_widen(__ldg(reinterpret_cast<const uint4 *>(DHO + (t * N + j) * d + k)), gr);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) dot(hv[i], gr, acc[i * N + j]);
+                        dot(hv[N], gr, acc[Q::B + j]);
+                    }
+                }
+            }
+            warp_sums_all<NV>(acc, red + warp * NV, lane);
+            __syncthreads();
+            if (warp == 0) ck_finish_sums<N>(red, nwarps, fin, stat, d, p.eps, lane);
+            __syncthreads();
+            if (warp == 0) ck_write_params<N>(fin, stat, At, bt, at, bp.gA, bp.gb, bp.ga, t, lane);
+
+            // ---- pass 2: the gradients of H and y ----
+            const float2 r2 = make_float2(stat[0], stat[0]), nq2 = make_float2(-stat[1], -stat[1]);
+            for (int64_t c = tid; c < nvec; c += NT) {
+                const int64_t k = c * V;
+                float2 dx[VP], gv[VP], h[VP], dh[VP];
+                ck_widen(__ldcs(reinterpret_cast<const uint4 *>(DX + t * d + k)), dx);
+                load_gain2<VP>(p.g, k, gv);
+                if constexpr (PARK) {
+#pragma unroll
+                    for (int e = 0; e < VP; e += 2) {
+                        const float4 f = *reinterpret_cast<const float4 *>(shp + k + 2 * e);
+                        h[e] = make_float2(f.x, f.y);
+                        h[e + 1] = make_float2(f.z, f.w);
+                    }
+                } else {
+                    float2 hv[N + 1][VP];
+                    load_kept(k, hv);
+                    mix_h(hv, h);
+                }
+#pragma unroll
+                for (int e = 0; e < VP; ++e) dh[e] = ffma2_rn(nq2, h[e], fmul2_rn(r2, fmul2_rn(dx[e], gv[e])));
+                if (sdg) {
+#pragma unroll
+                    for (int e = 0; e < VP; e += 2) {
+                        float4 *pd = reinterpret_cast<float4 *>(sdg + k + 2 * e);
+                        const float4 f = *pd;
+                        const float2 s0 = ffma2_rn(fmul2_rn(dx[e], h[e]), r2, make_float2(f.x, f.y));
+                        const float2 s1 = ffma2_rn(fmul2_rn(dx[e + 1], h[e + 1]), r2, make_float2(f.z, f.w));
+                        *pd = make_float4(s0.x, s0.y, s1.x, s1.y);
+                    }
+                }
+                float2 o[N + 1][VP];
+#pragma unroll
+                for (int i = 0; i <= N; ++i)
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) o[i][e] = fmul2_rn(make_float2(ct[i], ct[i]), dh[e]);
+                if (DHO) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        float2 gr[VP];
+                        ck_widen(__ldcs(reinterpret_cast<const uint4 *>(DHO + (t * N + j) * d + k)), gr);
+#pragma unroll
+                        for (int i = 0; i <= N; ++i) {
+                            const float w = i < N ? At[i * N + j] : bt[j];
+#pragma unroll
+                            for (int e = 0; e < VP; ++e) o[i][e] = ffma2_rn(make_float2(w, w), gr[e], o[i][e]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    __stcs(reinterpret_cast<uint4 *>(DH + (t * N + i) * d + k), ck_narrow(o[i]));
+                __stcs(reinterpret_cast<uint4 *>(DY + t * d + k), ck_narrow(o[N]));
+            }
+        }
+    }
+}
+
+template <int N, typename S>
+struct CkBw {
+    static constexpr int V = StorageTraits<S>::V;
+    // h parked up to 96 KB of d: two CTAs a multiprocessor at n <= 4
+    static bool parked(int64_t d) { return d * 4 <= 96 * 1024; }
+    static int threads(int64_t d) {
+        const int64_t nvec = d / V;
+        int64_t nt = nvec < kThreads ? (nvec + 31) / 32 * 32 : kThreads;
+        // a size that divides the row's slices, when one is near the largest
+        for (int64_t c = nt; c >= nt / 2 && c >= 32 && nvec >= kThreads; c -= 32)
+            if (nvec % c == 0) return (int)c;
+        return (int)nt;
+    }
+    template <bool PARK>
+    static hc_status occupancy(int NT, size_t dyn, int &per_sm) {
+        auto kern = hc_ck_bwd_kernel<N, S, PARK>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, NT, dyn);
+        if (e != cudaSuccess)
+            return set_error(HC_ERR_CUDA, "checkpoint backward occupancy: %s", cudaGetErrorString(e));
+        return HC_OK;
+    }
+    static hc_status grid(int64_t T, int64_t d, const LaunchCtx &ctx, int64_t &grid) {
+        int per_sm = 0;
+        const int NT = threads(d);
+        const hc_status s = parked(d) ? occupancy<true>(NT, (size_t)d * 4, per_sm) : occupancy<false>(NT, 0, per_sm);
+        if (s != HC_OK) return s;
+        grid = (int64_t)ctx.sms * (per_sm < 1 ? 1 : per_sm);
+        if (grid > T) grid = T;
+        return HC_OK;
+    }
+    static hc_status launch(const BackwardArgs &a, const uint8_t *sH, const uint8_t *sy, int64_t g,
+                            cudaStream_t st) {
+        CkBwParams bp{};
+        bp.f = a.f;
+        bp.sH = sH;
+        bp.sy = sy;
+        bp.ns = ck_scale_stride(a.f.d);
+        bp.dHout = a.dHout;
+        bp.dx = a.dx;
+        bp.dH = a.dH;
+        bp.dy = a.dy;
+        bp.gA = a.dA;
+        bp.gb = a.db;
+        bp.ga = a.da;
+        bp.dg_part = a.dg ? static_cast<float *>(a.workspace) : nullptr;
+        const int NT = threads(a.f.d);
+        if (parked(a.f.d)) hc_ck_bwd_kernel<N, S, true><<<(unsigned)g, NT, (size_t)a.f.d * 4, st>>>(bp);
+        else hc_ck_bwd_kernel<N, S, false><<<(unsigned)g, NT, 0, st>>>(bp);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "hc_ck_bwd_kernel launch: %s", cudaGetErrorString(e));
+        return HC_OK;
+    }
+};
+
+template <int N>
+hc_status grid_n(hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx, int64_t &g) {
+    return dt == HC_BF16 ? CkBw<N, __nv_bfloat16>::grid(T, d, ctx, g) : CkBw<N, float>::grid(T, d, ctx, g);
+}
+template <int N>
+hc_status launch_n(const BackwardArgs &a, const uint8_t *sH, const uint8_t *sy, int64_t g, cudaStream_t st) {
+    return a.dt == HC_BF16 ? CkBw<N, __nv_bfloat16>::launch(a, sH, sy, g, st)
+                           : CkBw<N, float>::launch(a, sH, sy, g, st);
+}
+
+hc_status grid_of(int n, hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx, int64_t &g) {
+    switch (n) {
+        case 1: return grid_n<1>(dt, T, d, ctx, g);
+        case 2: return grid_n<2>(dt, T, d, ctx, g);
+        case 3: return grid_n<3>(dt, T, d, ctx, g);
+        case 4: return grid_n<4>(dt, T, d, ctx, g);
+        case 5: return grid_n<5>(dt, T, d, ctx, g);
+        case 6: return grid_n<6>(dt, T, d, ctx, g);
+        case 7: return grid_n<7>(dt, T, d, ctx, g);
+        default: return grid_n<8>(dt, T, d, ctx, g);
+    }
+}
+
+}  // namespace
+
+hc_status checkpoint_backward_workspace_bytes(int n, hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx,
+                                              size_t *bytes) {
+    int64_t g = 0;
+    const hc_status s = grid_of(n, dt, T, d, ctx, g);
+    if (s != HC_OK) return s;
+    *bytes = (size_t)g * (size_t)d * sizeof(float);
+    return HC_OK;
+}
+
+hc_status launch_checkpoint_backward(const BackwardArgs &a, const uint8_t *sH, const uint8_t *sy,
+                                     const LaunchCtx &ctx, cudaStream_t st) {
+    hc_status s = check_param_backward(a);
+    if (s != HC_OK) return s;
+    int64_t g = 0;
+    s = grid_of(a.n, a.dt, a.f.T, a.f.d, ctx, g);
+    if (s != HC_OK) return s;
+    const size_t need = (size_t)g * (size_t)a.f.d * sizeof(float);
+    if (a.dg && a.workspace_bytes < need)
+        return set_error(HC_ERR_INVALID_ARG, "workspace of %zu bytes < %zu needed for dg", a.workspace_bytes, need);
+    switch (a.n) {
+        case 1: s = launch_n<1>(a, sH, sy, g, st); break;
+        case 2: s = launch_n<2>(a, sH, sy, g, st); break;
+        case 3: s = launch_n<3>(a, sH, sy, g, st); break;
+        case 4: s = launch_n<4>(a, sH, sy, g, st); break;
+        case 5: s = launch_n<5>(a, sH, sy, g, st); break;
+        case 6: s = launch_n<6>(a, sH, sy, g, st); break;
+        case 7: s = launch_n<7>(a, sH, sy, g, st); break;
+        default: s = launch_n<8>(a, sH, sy, g, st); break;
+    }
+    if (s != HC_OK) return s;
+    return launch_backward_tail(a, g, ctx, st);
+}
+
+}  // namespace hc

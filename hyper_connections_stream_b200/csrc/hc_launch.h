@@ -70,6 +70,42 @@ hc_status backward_workspace_bytes(int n, hc_dtype dt, int64_t T, int64_t d, con
                                    size_t *bytes);
 hc_status launch_backward(const BackwardArgs &a, const LaunchCtx &ctx, cudaStream_t st);
 
+// The part of a backward after the streams' kernel: refused (before any
+// launch) when the Sinkhorn iterates do not fit; then the softmax and Sinkhorn
+// backward in place on a.da and a.dA, and a.dg from `rows` rows of a.workspace.
+hc_status check_param_backward(const BackwardArgs &a);
+hc_status launch_backward_tail(const BackwardArgs &a, int64_t rows, const LaunchCtx &ctx, cudaStream_t st);
+
+// 8-bit checkpoints (hc_checkpoint.cuh): rows of d values to codes and
+// exponents and back, and the step's backward from those of H and y (a.f.H and
+// a.f.y hold the codes).
+hc_status launch_checkpoint_pack(const void *X, hc_dtype dt, uint8_t *q, uint8_t *s, int64_t rows, int64_t d,
+                                 const LaunchCtx &ctx, cudaStream_t st);
+hc_status launch_checkpoint_unpack(const uint8_t *q, const uint8_t *s, void *X, hc_dtype dt, int64_t rows, int64_t d,
+                                   const LaunchCtx &ctx, cudaStream_t st);
+hc_status checkpoint_backward_workspace_bytes(int n, hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx,
+                                              size_t *bytes);
+hc_status launch_checkpoint_backward(const BackwardArgs &a, const uint8_t *sH, const uint8_t *sy,
+                                     const LaunchCtx &ctx, cudaStream_t st);
+
+// The read with layer norm, and its gradients (see hc_read_layernorm).
+struct LayerNormArgs {
+    StepParams f;         // H (rows of dt, or codes), x, a (null: weight 1, n == 1), g, eps, T, d
+    int n;
+    hc_dtype dt;
+    const float *beta;    // forward
+    const uint8_t *sH;    // backward: exponents of a checkpoint, or null when H holds rows of dt
+    const void *dx;
+    void *dH;
+    float *da, *dg, *dbeta;  // each may be null
+    void *workspace;
+    size_t workspace_bytes;
+};
+hc_status launch_layernorm(const LayerNormArgs &a, const LaunchCtx &ctx, cudaStream_t st);
+hc_status layernorm_backward_workspace_bytes(int n, hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx,
+                                             size_t *bytes);
+hc_status launch_layernorm_backward(const LayerNormArgs &a, const LaunchCtx &ctx, cudaStream_t st);
+
 // The write mix fused with the tensor-parallel all-reduce of y, then the
 // next layer's read (see hc_reduce_write_then_read).
 constexpr int kMaxRanks = 8;

@@ -308,6 +308,101 @@ HC_API hc_status hc_write_then_read_backward_noalloc(
     float *dg, hc_stream stream);
 
 /*
+ * 8-bit checkpoints of the streams (training): what the backward of a step
+ * needs of the forward, kept at 1 + 1/32 bytes a value. The pages have no
+ * counterpart to these.
+ *   Rows of d values; blocks of 32 along d (the last one of a row may be
+ *   shorter). A block's scale is 2^e, e the smallest exponent with
+ *   max|x| / 2^e <= 448 over the block's finite values, at least -126; a value
+ *   is kept as the e4m3 code of x / 2^e (round to nearest even; nothing
+ *   saturates). The kept value, code * 2^e, is exact in bf16 and fp32 except
+ *   below the type's smallest normal. A value that is not finite is kept as
+ *   NaN and does not move its block's scale; a block of zeros has e = -126.
+ *   codes  [rows][d], one byte a value (e4m3);
+ *   scales [rows][hc_checkpoint_scale_stride(d)], e + 127 in one byte a block,
+ *          rows padded to 16 bytes; the padding is neither written nor read.
+ *   Both 16-byte aligned. For streams H rows = T * n, for a block output T.
+ *
+ * hc_checkpoint_pack: X [rows][d] (dt) to codes and scales.
+ * hc_checkpoint_unpack: the kept values to X [rows][d] (dt).
+ * No output may overlap an input or another output. d <= 2^30. Asynchronous;
+ * rows == 0 is a no-op.
+ */
+HC_API int64_t hc_checkpoint_scale_stride(int64_t d);
+HC_API hc_status hc_checkpoint_pack(const void *X, hc_dtype dt, int64_t rows, int64_t d, uint8_t *codes,
+                                    uint8_t *scales, hc_stream stream);
+HC_API hc_status hc_checkpoint_unpack(const uint8_t *codes, const uint8_t *scales, void *X, hc_dtype dt,
+                                      int64_t rows, int64_t d, hc_stream stream);
+
+/*
+ * hc_write_then_read that also keeps a checkpoint of its H and y for
+ * hc_write_then_read_backward_checkpoint. Hout and x_next are those of
+ * hc_write_then_read bit for bit, the checkpoints those of hc_checkpoint_pack
+ * of H and y as they were before the call (Hout == H is allowed). Other
+ * arguments and checks as hc_write_then_read; no output may overlap an input
+ * or another output.
+ */
+HC_API hc_status hc_write_then_read_checkpoint(
+    const void *H, const void *y, void *Hout, void *x_next, hc_dtype dt, int64_t T, int n, int64_t d,
+    hc_mix_mode mm, const float *A, int64_t A_tok_stride, int K, const float *b, int64_t b_tok_stride,
+    hc_read_mode rm, const float *a_next, int64_t a_tok_stride, const float *g_next, float eps, uint8_t *H_codes,
+    uint8_t *H_scales, uint8_t *y_codes, uint8_t *y_scales, hc_stream stream);
+
+/*
+ * Backward of hc_write_then_read from the checkpoint of its H and y: the
+ * gradients of the step at the kept values, with H' not rounded to dt between
+ * the write and the read (the kept values' own rounding is 2^-4, and the
+ * gradients pass straight through every rounding). dt is the type of dHout,
+ * dx, dH and dy. Arguments, outputs and the workspace rule (its size from
+ * hc_write_then_read_backward_checkpoint_workspace_bytes) otherwise as
+ * hc_write_then_read_backward. At n = 1 the norm cancels the read weight: its
+ * gradient is rounding. T == 0 sets dg (if given) to zero and does nothing
+ * else.
+ */
+HC_API hc_status hc_write_then_read_backward_checkpoint(
+    const uint8_t *H_codes, const uint8_t *H_scales, const uint8_t *y_codes, const uint8_t *y_scales, hc_dtype dt,
+    int64_t T, int n, int64_t d, hc_mix_mode mm, const float *A, int64_t A_tok_stride, int K, const float *b,
+    int64_t b_tok_stride, hc_read_mode rm, const float *a, int64_t a_tok_stride, const float *g, float eps,
+    const void *dHout, const void *dx, void *dH, void *dy, float *dA, float *db, float *da, float *dg,
+    void *workspace, size_t workspace_bytes, hc_stream stream);
+HC_API size_t hc_write_then_read_backward_checkpoint_workspace_bytes(hc_dtype dt, int64_t T, int n, int64_t d);
+
+/*
+ * Read mix followed by a layer norm, for blocks whose pre-norm subtracts the
+ * mean (the pages' blocks use RMSNorm, hc_read_rmsnorm; this is the other
+ * common pre-norm):
+ *   h = sum_i a_i H_i,  x = (h - mean(h)) / sqrt(mean((h - mean(h))^2) + eps) * g + beta
+ *   beta: [d] fp32 or NULL for none, 16-byte aligned.
+ *   a may be NULL when n == 1: weight 1, the plain layer norm of rows [T][d].
+ * Other arguments as hc_read_rmsnorm. h in fp32, the moments in fp64 over
+ * fp32 sums about a pivot, x rounded once.
+ */
+HC_API hc_status hc_read_layernorm(const void *H, void *x, hc_dtype dt, int64_t T, int n, int64_t d,
+                                   hc_read_mode rm, const float *a, int64_t a_tok_stride, const float *g,
+                                   const float *beta, float eps, hc_stream stream);
+
+/*
+ * Backward of hc_read_layernorm.
+ *   H: the forward's streams (dt), or with H_scales not NULL the codes of
+ *     their checkpoint (the gradients are then those at the kept values).
+ *   dx [T][d] (dt): gradient arriving at x. dH [T][n][d] (dt) out.
+ *   da [T][n] fp32: per-token gradients w.r.t. the read logits when
+ *     rm == HC_READ_SOFTMAX_LOGITS, else the weights; NULL for none; needs a.
+ *   dg (needs g), dbeta [d] fp32: summed over tokens in a fixed order; each
+ *     NULL for none. Either needs a workspace of
+ *     hc_read_layernorm_backward_workspace_bytes() bytes, 16-byte aligned.
+ * At n = 1 the norm cancels the read weight: its gradient is rounding. No
+ * output may overlap an input or another output. T == 0 sets dg and dbeta (if
+ * given) to zero and does nothing else.
+ */
+HC_API hc_status hc_read_layernorm_backward(const void *H, const uint8_t *H_scales, hc_dtype dt, int64_t T, int n,
+                                            int64_t d, hc_read_mode rm, const float *a, int64_t a_tok_stride,
+                                            const float *g, float eps, const void *dx, void *dH, float *da,
+                                            float *dg, float *dbeta, void *workspace, size_t workspace_bytes,
+                                            hc_stream stream);
+HC_API size_t hc_read_layernorm_backward_workspace_bytes(hc_dtype dt, int64_t T, int n, int64_t d);
+
+/*
  * Ends of a stack ("Tencent open-sources Hy4 Preview at 770B -- Identity
  * Hyper-Connections", learnaivisually: TL;DR and the residual-design table --
  * the n streams start as copies of one; the pages do not say how they are
