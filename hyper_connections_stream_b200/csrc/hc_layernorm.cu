@@ -19,7 +19,10 @@
 // and beta accumulate in the CTA's workspace row and are summed over the rows
 // in a fixed order.
 #include "hc_checkpoint.cuh"
+#include <atomic>
+
 #include "hc_launch.h"
+#include "hc_sync.cuh"
 #include "hc_token_sums.cuh"
 
 namespace hc {
@@ -332,6 +335,333 @@ hc_layernorm_bwd_kernel(LnBwParams bp) {
     }
 }
 
+// ---- token ring ------------------------------------------------------------------
+// A producer warp moves whole tokens (H's rows or codes and exponents, dx) into
+// a ring of stages with bulk copies and leaves the token's read weights beside
+// them; NG groups of gw warps take the CTA's tokens in turn, so one group's
+// exchanges and stores overlap the other's loads from shared memory. A thread
+// owns up to kCPT slices of 16 bytes of dx, the same columns for every token,
+// so the gradients of g and beta stay in its registers; they are added over
+// the groups in shared memory at the end (in group order) and leave one row a
+// CTA. A token takes two exchanges: the sum of h, then the sums about that
+// mean (with the sum of h - mean itself, which corrects the mean's rounding).
+//
+// Every wait is bounded (hc_sync.cuh); on time-out the fault code is recorded
+// and the CTA runs to its end without waiting again (its results are void, its
+// accesses stay in bounds).
+constexpr int kCPT = 4;
+constexpr int kRingWarps = 14;   // consumer warps at most (128 registers a thread)
+
+struct LnRingShape {
+    int gw, ng, nst;
+    int stage_bytes;
+};
+
+__host__ __device__ inline int64_t ln_ring_fixed_bytes(int n, int64_t d, int ng, int nst) {
+    return d * 4 + ng * d * 4                         // g, parked h
+           + (int64_t)nst * (kMaxStreams * 4 + 16)    // weights, barriers
+           + (int64_t)kRingWarps * (4 + 16 + n * 4) + 32;  // sums, abort flag
+}
+
+__device__ __forceinline__ void group_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+template <int N, typename S, bool PACKED>
+__global__ void __launch_bounds__(32 * (kRingWarps + 1), 1)
+hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
+    const StepParams &p = bp.f;
+    constexpr int V = StorageTraits<S>::V, VP = V / 2;
+    const int d = (int)p.d, ns = (int)bp.ns, nst = sh.nst, GW = sh.gw, NG = sh.ng;
+    const int64_t G = gridDim.x;
+    const int64_t M = (p.T > (int64_t)blockIdx.x) ? (p.T - 1 - blockIdx.x) / G + 1 : 0;
+    const int rb = d * (int)sizeof(S), o_sc = N * d, o_dx = PACKED ? N * (d + ns) : N * rb;
+
+    extern __shared__ __align__(128) unsigned char smem[];
+    float *sg = reinterpret_cast<float *>(smem + (int64_t)nst * sh.stage_bytes);  // [d]
+    float *hrow = sg + d;                                                          // [NG][d]
+    float *wts = hrow + (int64_t)NG * d;                                           // [nst][8]
+    float *red4 = wts + nst * kMaxStreams;                                         // [warps][4]
+    float *red1 = red4 + kRingWarps * 4;                                           // [warps]
+    float *dred = red1 + kRingWarps;                                               // [warps][N]
+    uint64_t *full = reinterpret_cast<uint64_t *>(dred + (kRingWarps * N + 1) / 2 * 2);
+    uint64_t *empty = full + nst;
+    int *abort_word = reinterpret_cast<int *>(empty + nst);
+    volatile int *abort_flag = abort_word;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < nst; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], GW);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    for (int k = threadIdx.x; k < d; k += blockDim.x) sg[k] = p.g ? p.g[k] : 1.0f;
+    __syncthreads();
+
+    if (warp == NG * GW) {
+        // ---------------- producer ----------------
+        const S *DX = static_cast<const S *>(bp.dx);
+        auto weight = [&](int64_t m) {
+            return p.a && lane < N && m < M ? __ldg(p.a + (blockIdx.x + m * G) * p.a_s + lane) : 1.0f;
+        };
+        float next = weight(0);
+        int s = 0;
+        uint32_t ph = 1;  // parity of the stage's previous release
+        int64_t m = 0;
+        for (; m < M; ++m) {
+            const int64_t t = blockIdx.x + m * G;
+            bool ok = true;
+            if (m >= nst) ok = mbar_wait_bounded(&empty[s], ph, abort_flag, fault, FAULT_WAIT_EMPTY);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            unsigned char *st = smem + (int64_t)s * sh.stage_bytes;
+            float w = next;
+            next = weight(m + 1);
+            if (p.read_logits) {  // softmax over the n logits, in index order
+                float mx = __shfl_sync(0xffffffffu, w, 0);
+#pragma unroll
+                for (int x = 1; x < N; ++x) {
+                    const float v = __shfl_sync(0xffffffffu, w, x);
+                    if (v > mx) mx = v;
+                }
+                const float e = expf(__fsub_rn(w, mx));
+                float sum = 0.0f;
+#pragma unroll
+                for (int x = 0; x < N; ++x) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, e, x));
+                w = __fdiv_rn(e, sum);
+            }
+            if (lane < N) wts[s * kMaxStreams + lane] = w;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&full[s], (uint32_t)sh.stage_bytes);
+                if constexpr (PACKED) {
+                    bulk_load(st, static_cast<const uint8_t *>(p.H) + t * N * d, (uint32_t)(N * d), &full[s]);
+                    bulk_load(st + o_sc, bp.sH + t * N * ns, (uint32_t)(N * ns), &full[s]);
+                } else {
+                    bulk_load(st, static_cast<const S *>(p.H) + t * N * d, (uint32_t)(N * rb), &full[s]);
+                }
+                bulk_load(st + o_dx, DX + t * d, (uint32_t)rb, &full[s]);
+            }
+            if (++s == nst) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        // every issued copy lands before the CTA may exit (normally already done)
+        if (lane == 0)
+            for (int64_t q = (m > nst ? m - nst : 0); q < m; ++q)
+                mbar_wait_drain(&full[(int)(q % nst)], (uint32_t)((q / nst) & 1), fault);
+        return;
+    }
+
+    // ---------------- consumers ----------------
+    const int g = warp / GW, gw = warp - g * GW, gt = gw * 32 + lane, GT = GW * 32;
+    const int k0 = gt * V, kstep = GT * V;
+    float *hr = hrow + (int64_t)g * d;
+    float *r4 = red4 + g * GW * 4, *r1 = red1 + g * GW, *dr = dred + g * GW * N;
+    S *DH = static_cast<S *>(bp.dH);
+    float2 ag[kCPT][VP], ab[kCPT][VP];  // gradients of g and beta
+#pragma unroll
+    for (int u = 0; u < kCPT; ++u)
+#pragma unroll
+        for (int e = 0; e < VP; ++e) ag[u][e] = ab[u][e] = make_float2(0.0f, 0.0f);
+    const float inv_d = 1.0f / (float)d;
+
+    auto load_row = [&](const unsigned char *st, int x, int k, float2 (&v)[VP]) {
+        if constexpr (PACKED) {
+            uint32_t q[V / 4];
+            if constexpr (V == 8) {
+                const uint2 c = *reinterpret_cast<const uint2 *>(st + x * d + k);
+                q[0] = c.x;
+                q[1] = c.y;
+            } else {
+                q[0] = *reinterpret_cast<const uint32_t *>(st + x * d + k);
+            }
+            ck_decode<VP>(q, ck_scale(st[o_sc + x * ns + k / kCkBlock]), v);
+        } else {
+            ck_widen(*reinterpret_cast<const uint4 *>(st + x * rb + k * (int)sizeof(S)), v);
+        }
+    };
+    auto load_f32 = [&](const float *q, float2 (&v)[VP]) {
+#pragma unroll
+        for (int e = 0; e < VP; e += 2) {
+            const float4 f = *reinterpret_cast<const float4 *>(q + 2 * e);
+            v[e] = make_float2(f.x, f.y);
+            v[e + 1] = make_float2(f.z, f.w);
+        }
+    };
+    // the last token's da, once its group's warps have met at a barrier
+    float a_prev = 0.0f;
+    auto write_da = [&](int64_t t) {
+        float sum = 0.0f;
+        if (lane < N)
+            for (int w = 0; w < GW; ++w) sum += dr[w * N + lane];
+        if (p.read_logits) {  // through the softmax: a (da - sum a da)
+            float dot = 0.0f;
+#pragma unroll
+            for (int x = 0; x < N; ++x) dot += __shfl_sync(0xffffffffu, a_prev * sum, x);
+            sum = a_prev * (sum - dot);
+        }
+        if (lane < N) bp.da[t * N + lane] = sum;
+    };
+
+    int64_t t_prev = -1;
+    for (int64_t m = g; m < M; m += NG) {
+        const int64_t t = blockIdx.x + m * G;
+        const int s = (int)(m % nst);
+        mbar_wait_bounded(&full[s], (uint32_t)((m / nst) & 1), abort_flag, fault, FAULT_WAIT_FULL);
+        const unsigned char *st = smem + (int64_t)s * sh.stage_bytes;
+        const float *at = wts + s * kMaxStreams;
+
+        // h, parked, and its sum
+        float sum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kCPT; ++u) {
+            const int k = k0 + u * kstep;
+            if (k < d) {
+                float2 h[VP];
+#pragma unroll
+                for (int x = 0; x < N; ++x) {
+                    float2 v[VP];
+                    load_row(st, x, k, v);
+                    const float2 ax = make_float2(at[x], at[x]);
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) h[e] = x == 0 ? fmul2_rn(ax, v[e]) : ffma2_rn(ax, v[e], h[e]);
+                }
+                float2 z = h[0];
+#pragma unroll
+                for (int e = 1; e < VP; ++e) z = fadd2_rn(z, h[e]);
+                sum += z.x + z.y;
+#pragma unroll
+                for (int e = 0; e < VP; e += 2)
+                    *reinterpret_cast<float4 *>(hr + k + 2 * e) = make_float4(h[e].x, h[e].y, h[e + 1].x, h[e + 1].y);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) r1[gw] = sum;
+        group_sync(1 + g, GT);
+        if (bp.da && gw == 0 && t_prev >= 0) write_da(t_prev);
+        if (lane < N) a_prev = at[lane];
+        float mean = 0.0f;
+        for (int w = 0; w < GW; ++w) mean += r1[w];
+        mean *= inv_d;
+
+        // sums about the mean: h - mean, its square, u, u (h - mean)
+        const float2 nm = make_float2(-mean, -mean);
+        {
+            float2 s0 = make_float2(0.f, 0.f), s1 = s0, s2 = s0, s3 = s0;
+#pragma unroll
+            for (int u = 0; u < kCPT; ++u) {
+                const int k = k0 + u * kstep;
+                if (k < d) {
+                    float2 h[VP], dx[VP], gv[VP];
+                    load_f32(hr + k, h);
+                    load_f32(sg + k, gv);
+                    ck_widen(*reinterpret_cast<const uint4 *>(st + o_dx + k * (int)sizeof(S)), dx);
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) {
+                        const float2 c = fadd2_rn(h[e], nm), w = fmul2_rn(dx[e], gv[e]);
+                        s0 = fadd2_rn(s0, c);
+                        s1 = ffma2_rn(c, c, s1);
+                        s2 = fadd2_rn(s2, w);
+                        s3 = ffma2_rn(w, c, s3);
+                    }
+                }
+            }
+            const float v[4] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, s3.x + s3.y};
+            bw_warp_sums_to<4>(v, r4 + gw * 4, lane);
+        }
+        group_sync(1 + g, GT);
+        float4 tot = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < GW; ++w) {
+            const float4 f = *reinterpret_cast<const float4 *>(r4 + w * 4);
+            tot.x += f.x; tot.y += f.y; tot.z += f.z; tot.w += f.w;
+        }
+        const float off = tot.x * inv_d;  // what the mean lacks
+        const float var = fmaxf(__fmaf_rn(-off, off, tot.y * inv_d), 0.0f);
+        const float rs = tot.y == tot.y ? __frsqrt_rn(var + p.eps) : tot.y;  // fmaxf drops a NaN
+        const float c1 = tot.z * inv_d, c2 = rs * (tot.w - off * tot.z) * inv_d;
+        const float2 no = make_float2(-off, -off), r2 = make_float2(rs, rs);
+        const float2 n1 = make_float2(-c1, -c1), n2 = make_float2(-c2, -c2);
+
+        // the gradients
+        float dacc[N];
+#pragma unroll
+        for (int x = 0; x < N; ++x) dacc[x] = 0.0f;
+        S *DHt = DH + t * N * d;
+#pragma unroll
+        for (int u = 0; u < kCPT; ++u) {
+            const int k = k0 + u * kstep;
+            if (k < d) {
+                float2 z[VP], dx[VP], dh[VP];
+                load_f32(hr + k, z);
+                load_f32(sg + k, dh);
+                ck_widen(*reinterpret_cast<const uint4 *>(st + o_dx + k * (int)sizeof(S)), dx);
+#pragma unroll
+                for (int e = 0; e < VP; ++e) {
+                    z[e] = fmul2_rn(fadd2_rn(fadd2_rn(z[e], nm), no), r2);
+                    ag[u][e] = ffma2_rn(dx[e], z[e], ag[u][e]);
+                    ab[u][e] = fadd2_rn(dx[e], ab[u][e]);
+                    dh[e] = fmul2_rn(ffma2_rn(n2, z[e], fadd2_rn(fmul2_rn(dx[e], dh[e]), n1)), r2);
+                }
+#pragma unroll
+                for (int x = 0; x < N; ++x) {
+                    float2 o[VP];
+                    const float2 ax = make_float2(at[x], at[x]);
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) o[e] = fmul2_rn(ax, dh[e]);
+                    if (bp.da) {
+                        float2 v[VP];
+                        load_row(st, x, k, v);
+                        float2 q = fmul2_rn(dh[0], v[0]);
+#pragma unroll
+                        for (int e = 1; e < VP; ++e) q = ffma2_rn(dh[e], v[e], q);
+                        dacc[x] += q.x + q.y;
+                    }
+                    __stcs(reinterpret_cast<uint4 *>(DHt + x * d + k), ck_narrow(o));
+                }
+            }
+        }
+        if (bp.da) bw_warp_sums_to<N>(dacc, dr + gw * N, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        t_prev = t;
+    }
+    if (bp.da) {
+        group_sync(1 + g, GT);
+        if (gw == 0 && t_prev >= 0) write_da(t_prev);
+    }
+    if (bp.part) {
+        // the groups' sums, added in group order over the stages (all consumed)
+        float *acc = reinterpret_cast<float *>(smem);  // [2][d]
+        for (int q = 0; q < NG; ++q) {
+            group_sync(15, NG * GT);
+            if (q == g) {
+#pragma unroll
+                for (int u = 0; u < kCPT; ++u) {
+                    const int k = k0 + u * kstep;
+                    if (k < d) {
+#pragma unroll
+                        for (int e = 0; e < VP; ++e) {
+                            float2 *pg = reinterpret_cast<float2 *>(acc + k) + e;
+                            float2 *pb = reinterpret_cast<float2 *>(acc + d + k) + e;
+                            *pg = q == 0 ? ag[u][e] : fadd2_rn(*pg, ag[u][e]);
+                            *pb = q == 0 ? ab[u][e] : fadd2_rn(*pb, ab[u][e]);
+                        }
+                    }
+                }
+            }
+        }
+        group_sync(15, NG * GT);
+        float *row = bp.part + (int64_t)blockIdx.x * 2 * d;
+        for (int k = threadIdx.x * 4; k < 2 * d; k += NG * GT * 4)
+            *reinterpret_cast<float4 *>(row + k) = *reinterpret_cast<const float4 *>(acc + k);
+    }
+}
+
 // Sums over the rows of part [rows][cols] (fp64, 8 row slices in order):
 // columns below split to lo, the others to hi (either may be null).
 constexpr int kCols = 32, kSlices = 8;
@@ -414,20 +744,75 @@ struct LayerNorm {
         if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "layer norm occupancy: %s", cudaGetErrorString(e));
         return HC_OK;
     }
-    // The grid, which the workspace is sized by: the same whether H is packed.
-    static hc_status grid(int64_t T, int64_t d, const LaunchCtx &ctx, int64_t &g) {
-        int p0 = 0, p1 = 0;
-        hc_status s = occupancy<false>(d, p0);
-        if (s == HC_OK) s = occupancy<true>(d, p1);
-        if (s != HC_OK) return s;
-        const int per_sm = p0 < p1 ? p0 : p1;
+    // The ring's geometry, or gw = 0 where it does not apply: a group's warps
+    // must cover the row, at least two stages (and the final sums) must fit,
+    // and a checkpoint's codes must start on 16 bytes.
+    static LnRingShape ring(int64_t d, bool packed, int64_t &smem) {
+        LnRingShape sh{};
+        const int64_t nvec = d / V, gw = (nvec + 32 * kCPT - 1) / (32 * kCPT);
+        if (gw > kRingWarps || (packed && d % 16 != 0)) return sh;
+        const int64_t stage = N * (packed ? d + ck_scale_stride(d) : d * (int64_t)sizeof(S)) + d * (int64_t)sizeof(S);
+        for (int64_t ng = kRingWarps / gw; ng >= 1; --ng) {
+            int64_t nst = (kSmemLimitLogits - ln_ring_fixed_bytes(N, d, (int)ng, 0)) / (stage + kMaxStreams * 4 + 16);
+            if (nst < ng + 1 && !(ng == 1 && nst >= 2)) continue;
+            if (nst > 2 * ng + 2) nst = 2 * ng + 2;
+            if (nst * stage < 8 * d) continue;
+            sh.gw = (int)gw;
+            sh.ng = (int)ng;
+            sh.nst = (int)nst;
+            sh.stage_bytes = (int)stage;
+            smem = nst * stage + ln_ring_fixed_bytes(N, d, (int)ng, (int)nst);
+            break;
+        }
+        return sh;
+    }
+    // The grid, which the workspace is sized by: the larger of the two forms'.
+    static hc_status grid(int64_t T, int64_t d, bool packed, const LaunchCtx &ctx, int64_t &g) {
+        int64_t smem = 0;
+        int per_sm = 1;
+        if (!ring(d, packed, smem).gw) {
+            const hc_status s = packed ? occupancy<true>(d, per_sm) : occupancy<false>(d, per_sm);
+            if (s != HC_OK) return s;
+        }
         g = (int64_t)ctx.sms * (per_sm < 1 ? 1 : per_sm);
         if (g > T) g = T;
         return HC_OK;
     }
+    static hc_status workspace(int64_t T, int64_t d, const LaunchCtx &ctx, size_t *bytes) {
+        int64_t g0 = 0, g1 = 0;
+        hc_status s = grid(T, d, false, ctx, g0);
+        if (s == HC_OK) s = grid(T, d, true, ctx, g1);
+        if (s == HC_OK) *bytes = (size_t)(g0 > g1 ? g0 : g1) * 2 * (size_t)d * sizeof(float);
+        return s;
+    }
+    template <bool PACKED>
+    static hc_status launch_backward(const LnBwParams &bp, int64_t g, const LaunchCtx &ctx, cudaStream_t st) {
+        int64_t smem = 0;
+        const LnRingShape sh = ring(bp.f.d, PACKED, smem);
+        cudaError_t e;
+        if (sh.gw) {
+            auto kern = hc_layernorm_bwd_ring_kernel<N, S, PACKED>;
+            static std::atomic<int> configured[64];  // largest opt-in so far, per device
+            if (ctx.device < 0 || ctx.device >= 64)
+                return set_error(HC_ERR_UNSUPPORTED, "device ordinal %d >= 64", ctx.device);
+            if (smem > configured[ctx.device].load()) {
+                e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                if (e != cudaSuccess)
+                    return set_error(HC_ERR_CUDA, "layer norm smem attribute: %s", cudaGetErrorString(e));
+                configured[ctx.device].store((int)smem);
+            }
+            kern<<<(unsigned)g, 32 * (1 + sh.ng * sh.gw), (size_t)smem, st>>>(bp, sh, ctx.fault);
+        } else {
+            hc_layernorm_bwd_kernel<N, S, PACKED><<<(unsigned)g, threads(bp.f.d), (size_t)bp.f.d * 4, st>>>(bp);
+        }
+        e = cudaGetLastError();
+        if (e != cudaSuccess)
+            return set_error(HC_ERR_CUDA, "layer norm backward launch: %s", cudaGetErrorString(e));
+        return HC_OK;
+    }
     static hc_status backward(const LayerNormArgs &a, const LaunchCtx &ctx, cudaStream_t st) {
         int64_t g = 0;
-        const hc_status s = grid(a.f.T, a.f.d, ctx, g);
+        hc_status s = grid(a.f.T, a.f.d, a.sH != nullptr, ctx, g);
         if (s != HC_OK) return s;
         const bool want = a.dg || a.dbeta;
         const size_t need = (size_t)g * 2 * (size_t)a.f.d * sizeof(float);
@@ -442,17 +827,13 @@ struct LayerNorm {
         bp.dH = a.dH;
         bp.da = a.da;
         bp.part = want ? static_cast<float *>(a.workspace) : nullptr;
-        const int NT = threads(a.f.d);
-        if (a.sH) hc_layernorm_bwd_kernel<N, S, true><<<(unsigned)g, NT, (size_t)a.f.d * 4, st>>>(bp);
-        else hc_layernorm_bwd_kernel<N, S, false><<<(unsigned)g, NT, (size_t)a.f.d * 4, st>>>(bp);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess)
-            return set_error(HC_ERR_CUDA, "hc_layernorm_bwd_kernel launch: %s", cudaGetErrorString(e));
+        s = a.sH ? launch_backward<true>(bp, g, ctx, st) : launch_backward<false>(bp, g, ctx, st);
+        if (s != HC_OK) return s;
         if (want) {
             const int64_t cols = 2 * a.f.d;
             hc_colsum_kernel<<<(unsigned)((cols + kCols - 1) / kCols), kCols * kSlices, 0, st>>>(
                 static_cast<const float *>(a.workspace), (int)g, cols, a.f.d, a.dg, a.dbeta);
-            e = cudaGetLastError();
+            const cudaError_t e = cudaGetLastError();
             if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "hc_colsum_kernel launch: %s", cudaGetErrorString(e));
         }
         return HC_OK;
@@ -470,8 +851,9 @@ hc_status backward_n(const LayerNormArgs &a, const LaunchCtx &ctx, cudaStream_t 
                            : LayerNorm<N, float>::backward(a, ctx, st);
 }
 template <int N>
-hc_status grid_n(hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx, int64_t &g) {
-    return dt == HC_BF16 ? LayerNorm<N, __nv_bfloat16>::grid(T, d, ctx, g) : LayerNorm<N, float>::grid(T, d, ctx, g);
+hc_status workspace_n(hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx, size_t *bytes) {
+    return dt == HC_BF16 ? LayerNorm<N, __nv_bfloat16>::workspace(T, d, ctx, bytes)
+                         : LayerNorm<N, float>::workspace(T, d, ctx, bytes);
 }
 
 }  // namespace
@@ -491,21 +873,16 @@ hc_status launch_layernorm(const LayerNormArgs &a, const LaunchCtx &ctx, cudaStr
 
 hc_status layernorm_backward_workspace_bytes(int n, hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx,
                                              size_t *bytes) {
-    int64_t g = 0;
-    hc_status s;
     switch (n) {
-        case 1: s = grid_n<1>(dt, T, d, ctx, g); break;
-        case 2: s = grid_n<2>(dt, T, d, ctx, g); break;
-        case 3: s = grid_n<3>(dt, T, d, ctx, g); break;
-        case 4: s = grid_n<4>(dt, T, d, ctx, g); break;
-        case 5: s = grid_n<5>(dt, T, d, ctx, g); break;
-        case 6: s = grid_n<6>(dt, T, d, ctx, g); break;
-        case 7: s = grid_n<7>(dt, T, d, ctx, g); break;
-        default: s = grid_n<8>(dt, T, d, ctx, g); break;
+        case 1: return workspace_n<1>(dt, T, d, ctx, bytes);
+        case 2: return workspace_n<2>(dt, T, d, ctx, bytes);
+        case 3: return workspace_n<3>(dt, T, d, ctx, bytes);
+        case 4: return workspace_n<4>(dt, T, d, ctx, bytes);
+        case 5: return workspace_n<5>(dt, T, d, ctx, bytes);
+        case 6: return workspace_n<6>(dt, T, d, ctx, bytes);
+        case 7: return workspace_n<7>(dt, T, d, ctx, bytes);
+        default: return workspace_n<8>(dt, T, d, ctx, bytes);
     }
-    if (s != HC_OK) return s;
-    *bytes = (size_t)g * 2 * (size_t)d * sizeof(float);
-    return HC_OK;
 }
 
 hc_status launch_layernorm_backward(const LayerNormArgs &a, const LaunchCtx &ctx, cudaStream_t st) {
