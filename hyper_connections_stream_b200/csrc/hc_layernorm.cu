@@ -20,6 +20,7 @@
 // in a fixed order.
 #include "hc_checkpoint.cuh"
 #include <atomic>
+#include <type_traits>
 
 #include "hc_launch.h"
 #include "hc_sync.cuh"
@@ -338,29 +339,36 @@ hc_layernorm_bwd_kernel(LnBwParams bp) {
 // ---- token ring ------------------------------------------------------------------
 // A producer warp moves whole tokens (H's rows or codes and exponents, dx) into
 // a ring of stages with bulk copies and leaves the token's read weights beside
-// them; NG groups of gw warps take the CTA's tokens in turn, so one group's
-// exchanges and stores overlap the other's loads from shared memory. A thread
-// owns up to kCPT slices of 16 bytes of dx, the same columns for every token,
-// so the gradients of g and beta stay in its registers; they are added over
-// the groups in shared memory at the end (in group order) and leave one row a
-// CTA. A token takes two exchanges: the sum of h, then the sums about that
-// mean (with the sum of h - mean itself, which corrects the mean's rounding).
+// them; NG groups of gw warps take the CTA's tokens in turn. A thread owns up to
+// kCPT slices of 16 bytes of dx, the same columns for every token, so the
+// gradients of g and beta stay in its registers; they are added over the groups
+// in shared memory at the end (in group order) and leave one row a CTA.
+//
+// A token takes one exchange: every warp sums about its own mean, and the
+// statistic warp moves the warps' sums to the token's mean (Chan's formula; all
+// terms are differences of means, so a mean far from zero costs no accuracy,
+// and no exchange is needed to find it first). While it does, the group runs
+// the next token's first pass; the second pass of a token comes after that.
 //
 // Every wait is bounded (hc_sync.cuh); on time-out the fault code is recorded
 // and the CTA runs to its end without waiting again (its results are void, its
 // accesses stay in bounds).
-constexpr int kCPT = 4;
 constexpr int kRingWarps = 14;   // consumer warps at most (128 registers a thread)
+constexpr int kCPT = 2;          // slices a thread at most
 
 struct LnRingShape {
     int gw, ng, nst;
+    int nw;  // tokens whose weights are kept
     int stage_bytes;
 };
 
+// Floats of a group's exchange: two tokens' [4][32 warps] sums, [8] statistics,
+// [n][32 warps] da sums.
+__host__ __device__ constexpr int ln_red_floats(int n) { return 2 * (4 * 32 + 8 + n * 32); }
 __host__ __device__ inline int64_t ln_ring_fixed_bytes(int n, int64_t d, int ng, int nst) {
-    return d * 4 + ng * d * 4                         // g, parked h
-           + (int64_t)nst * (kMaxStreams * 4 + 16)    // weights, barriers
-           + (int64_t)kRingWarps * (4 + 16 + n * 4) + 32;  // sums, abort flag
+    return d * 4 + (int64_t)ng * ln_red_floats(n) * 4             // g, exchanges
+           + (int64_t)(nst + 2 * ng + 2) * kMaxStreams * 4        // weights
+           + (int64_t)nst * 16 + (int64_t)ng * 32 + 16;           // barriers, abort flag
 }
 
 __device__ __forceinline__ void group_sync(int id, int threads) {
@@ -368,10 +376,11 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
 }
 
 template <int N, typename S, bool PACKED>
-__global__ void __launch_bounds__(32 * (kRingWarps + 1), 1)
+__global__ void __launch_bounds__(32 * (kRingWarps + 2), 1)
 hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
     const StepParams &p = bp.f;
     constexpr int V = StorageTraits<S>::V, VP = V / 2;
+    constexpr int RF = ln_red_floats(N), kStat = 2 * 4 * 32, kDa = kStat + 2 * 8;
     const int d = (int)p.d, ns = (int)bp.ns, nst = sh.nst, GW = sh.gw, NG = sh.ng;
     const int64_t G = gridDim.x;
     const int64_t M = (p.T > (int64_t)blockIdx.x) ? (p.T - 1 - blockIdx.x) / G + 1 : 0;
@@ -379,14 +388,13 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
 
     extern __shared__ __align__(128) unsigned char smem[];
     float *sg = reinterpret_cast<float *>(smem + (int64_t)nst * sh.stage_bytes);  // [d]
-    float *hrow = sg + d;                                                          // [NG][d]
-    float *wts = hrow + (int64_t)NG * d;                                           // [nst][8]
-    float *red4 = wts + nst * kMaxStreams;                                         // [warps][4]
-    float *red1 = red4 + kRingWarps * 4;                                           // [warps]
-    float *dred = red1 + kRingWarps;                                               // [warps][N]
-    uint64_t *full = reinterpret_cast<uint64_t *>(dred + (kRingWarps * N + 1) / 2 * 2);
+    float *red = sg + d;                                                           // [NG][RF]
+    float *wts = red + NG * RF;                                                    // [nw][8]
+    uint64_t *full = reinterpret_cast<uint64_t *>(wts + sh.nw * kMaxStreams);
     uint64_t *empty = full + nst;
-    int *abort_word = reinterpret_cast<int *>(empty + nst);
+    uint64_t *sums = empty + nst;    // [NG][2]: the warps' sums of a token are there
+    uint64_t *stats = sums + 2 * NG;  // [NG][2]: its statistics are
+    int *abort_word = reinterpret_cast<int *>(stats + 2 * NG);
     volatile int *abort_flag = abort_word;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -395,11 +403,27 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], GW);
         }
+        for (int s = 0; s < 2 * NG; ++s) {
+            mbar_init(&sums[s], GW);
+            mbar_init(&stats[s], 1);
+        }
         *abort_flag = 0;
         fence_barrier_init();
     }
     for (int k = threadIdx.x; k < d; k += blockDim.x) sg[k] = p.g ? p.g[k] : 1.0f;
+    for (int k = threadIdx.x; k < NG * RF; k += blockDim.x) red[k] = 0.0f;  // a group may have fewer than 32 warps
     __syncthreads();
+    const float inv_d = 1.0f / (float)d;
+    // columns of warp w of a group
+    auto warp_columns = [&](int w) {
+        int n = 0;
+#pragma unroll
+        for (int u = 0; u < kCPT; ++u) {
+            const int left = d - (w + u * GW) * 32 * V;
+            n += left < 0 ? 0 : left < 32 * V ? left : 32 * V;
+        }
+        return n;
+    };
 
     if (warp == NG * GW) {
         // ---------------- producer ----------------
@@ -408,7 +432,7 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
             return p.a && lane < N && m < M ? __ldg(p.a + (blockIdx.x + m * G) * p.a_s + lane) : 1.0f;
         };
         float next = weight(0);
-        int s = 0;
+        int s = 0, sw = 0;
         uint32_t ph = 1;  // parity of the stage's previous release
         int64_t m = 0;
         for (; m < M; ++m) {
@@ -432,7 +456,7 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
                 for (int x = 0; x < N; ++x) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, e, x));
                 w = __fdiv_rn(e, sum);
             }
-            if (lane < N) wts[s * kMaxStreams + lane] = w;
+            if (lane < N) wts[sw * kMaxStreams + lane] = w;
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive_expect_tx(&full[s], (uint32_t)sh.stage_bytes);
@@ -448,6 +472,7 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
                 s = 0;
                 ph ^= 1u;
             }
+            if (++sw == sh.nw) sw = 0;
         }
         // every issued copy lands before the CTA may exit (normally already done)
         if (lane == 0)
@@ -456,18 +481,86 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
         return;
     }
 
+    if (warp == NG * GW + 1) {
+        // ---------------- statistics ----------------
+        const float n_w = lane < GW ? (float)warp_columns(lane) : 0.0f;  // lane w: warp w of the group
+        // da of the CTA's token m (of group gg), whose sums are in buffer par
+        auto write_da = [&](int64_t m, int gg, int par, int place) {
+            const float *dr = red + gg * RF + kDa + par * N * 32;
+            float sum = 0.0f;
+            if (lane < N) sum = sum16(dr + lane * 32) + sum16(dr + lane * 32 + 16);
+            if (p.read_logits) {  // through the softmax: a (da - sum a da)
+                const float w = lane < N ? wts[place * kMaxStreams + lane] : 0.0f;
+                float dot = 0.0f;
+#pragma unroll
+                for (int x = 0; x < N; ++x) dot += __shfl_sync(0xffffffffu, w * sum, x);
+                sum = w * (sum - dot);
+            }
+            if (lane < N) bp.da[(blockIdx.x + m * G) * N + lane] = sum;
+        };
+        int g = 0, par = 0, wo = 0;  // wo: place of the weights of the next da
+        uint32_t ph = 0;
+        for (int64_t m = 0; m < M; ++m) {
+            float *rq = red + g * RF + par * 4 * 32, *so = red + g * RF + kStat + par * 8;
+            mbar_wait_bounded(&sums[g * 2 + par], ph, abort_flag, fault, FAULT_WAIT_REDUCE);
+            // lane w: warp w's sums about its mean, moved to the mean of all
+            const float q = rq[lane], u = rq[32 + lane], z = rq[64 + lane];
+            const float m0 = rq[96], dm = n_w > 0.0f ? rq[96 + lane] - m0 : 0.0f;
+            float mu = n_w * dm, su = u;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                mu += __shfl_xor_sync(0xffffffffu, mu, o);
+                su += __shfl_xor_sync(0xffffffffu, su, o);
+            }
+            mu *= inv_d;  // the mean less m0
+            const float del = dm - mu;
+            float sq = __fmaf_rn(n_w * del, del, q), sz = __fmaf_rn(del, u, z);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                sz += __shfl_xor_sync(0xffffffffu, sz, o);
+            }
+            // dh = rs (u - c1 - c2 z), z = (h - mean) rs
+            const float rs = __frsqrt_rn(__fmaf_rn(sq, inv_d, p.eps));  // sq >= 0
+            const float c1 = su * inv_d, c2 = rs * sz * inv_d;
+            if (bp.da && m >= 2 * NG) {
+                write_da(m - 2 * NG, g, par, wo);
+                if (++wo == sh.nw) wo = 0;
+            }
+            if (lane == 0) {
+                *reinterpret_cast<float4 *>(so) = make_float4(m0, mu, rs, -rs * c1);
+                so[4] = -rs * c2;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&stats[g * 2 + par]);
+            if (++g == NG) {
+                g = 0;
+                ph ^= (uint32_t)par;
+                par ^= 1;
+            }
+        }
+        if (bp.da)  // the last two tokens of every group, after the group's last arrival
+            for (int64_t m = M > 2 * NG ? M - 2 * NG : 0; m < M; ++m) {
+                const int gg = (int)(m % NG);
+                const int64_t cnt = (M - 1 - gg) / NG + 1;  // the group's tokens; its last arrival is number cnt
+                mbar_wait_bounded(&sums[gg * 2 + (int)(cnt & 1)], (uint32_t)((cnt >> 1) & 1), abort_flag, fault,
+                                  FAULT_WAIT_REDUCE);
+                write_da(m, gg, (int)((m / NG) & 1), (int)(m % sh.nw));
+            }
+        return;
+    }
+
     // ---------------- consumers ----------------
-    const int g = warp / GW, gw = warp - g * GW, gt = gw * 32 + lane, GT = GW * 32;
-    const int k0 = gt * V, kstep = GT * V;
-    float *hr = hrow + (int64_t)g * d;
-    float *r4 = red4 + g * GW * 4, *r1 = red1 + g * GW, *dr = dred + g * GW * N;
+    const int g = warp / GW, gw = warp - g * GW, GT = GW * 32;
+    const int k0 = (gw * 32 + lane) * V, kstep = GT * V;  // this thread's columns
+    float *rg = red + g * RF;
     S *DH = static_cast<S *>(bp.dH);
     float2 ag[kCPT][VP], ab[kCPT][VP];  // gradients of g and beta
 #pragma unroll
     for (int u = 0; u < kCPT; ++u)
 #pragma unroll
         for (int e = 0; e < VP; ++e) ag[u][e] = ab[u][e] = make_float2(0.0f, 0.0f);
-    const float inv_d = 1.0f / (float)d;
+    const float inv_n = 1.0f / (float)warp_columns(gw);
 
     auto load_row = [&](const unsigned char *st, int x, int k, float2 (&v)[VP]) {
         if constexpr (PACKED) {
@@ -484,161 +577,154 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
             ck_widen(*reinterpret_cast<const uint4 *>(st + x * rb + k * (int)sizeof(S)), v);
         }
     };
-    auto load_f32 = [&](const float *q, float2 (&v)[VP]) {
+    auto load_gains = [&](int k, float2 (&v)[VP]) {
 #pragma unroll
         for (int e = 0; e < VP; e += 2) {
-            const float4 f = *reinterpret_cast<const float4 *>(q + 2 * e);
+            const float4 f = *reinterpret_cast<const float4 *>(sg + k + 2 * e);
             v[e] = make_float2(f.x, f.y);
             v[e + 1] = make_float2(f.z, f.w);
         }
     };
-    // the last token's da, once its group's warps have met at a barrier
-    float a_prev = 0.0f;
-    auto write_da = [&](int64_t t) {
-        float sum = 0.0f;
-        if (lane < N)
-            for (int w = 0; w < GW; ++w) sum += dr[w * N + lane];
-        if (p.read_logits) {  // through the softmax: a (da - sum a da)
-            float dot = 0.0f;
-#pragma unroll
-            for (int x = 0; x < N; ++x) dot += __shfl_sync(0xffffffffu, a_prev * sum, x);
-            sum = a_prev * (sum - dot);
-        }
-        if (lane < N) bp.da[t * N + lane] = sum;
-    };
 
-    int64_t t_prev = -1;
-    for (int64_t m = g; m < M; m += NG) {
-        const int64_t t = blockIdx.x + m * G;
-        const int s = (int)(m % nst);
-        mbar_wait_bounded(&full[s], (uint32_t)((m / nst) & 1), abort_flag, fault, FAULT_WAIT_FULL);
-        const unsigned char *st = smem + (int64_t)s * sh.stage_bytes;
-        const float *at = wts + s * kMaxStreams;
-
-        // h, parked, and its sum
-        float sum = 0.0f;
-#pragma unroll
-        for (int u = 0; u < kCPT; ++u) {
-            const int k = k0 + u * kstep;
-            if (k < d) {
-                float2 h[VP];
-#pragma unroll
-                for (int x = 0; x < N; ++x) {
-                    float2 v[VP];
-                    load_row(st, x, k, v);
-                    const float2 ax = make_float2(at[x], at[x]);
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) h[e] = x == 0 ? fmul2_rn(ax, v[e]) : ffma2_rn(ax, v[e], h[e]);
-                }
-                float2 z = h[0];
-#pragma unroll
-                for (int e = 1; e < VP; ++e) z = fadd2_rn(z, h[e]);
-                sum += z.x + z.y;
-#pragma unroll
-                for (int e = 0; e < VP; e += 2)
-                    *reinterpret_cast<float4 *>(hr + k + 2 * e) = make_float4(h[e].x, h[e].y, h[e + 1].x, h[e + 1].y);
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) r1[gw] = sum;
-        group_sync(1 + g, GT);
-        if (bp.da && gw == 0 && t_prev >= 0) write_da(t_prev);
-        if (lane < N) a_prev = at[lane];
-        float mean = 0.0f;
-        for (int w = 0; w < GW; ++w) mean += r1[w];
-        mean *= inv_d;
-
-        // sums about the mean: h - mean, its square, u, u (h - mean)
-        const float2 nm = make_float2(-mean, -mean);
-        {
-            float2 s0 = make_float2(0.f, 0.f), s1 = s0, s2 = s0, s3 = s0;
+    int slot = g % nst, slot0 = slot;        // stages of the token of the first and of the second pass
+    int ws = g % sh.nw, ws0 = ws;            // and places of their weights
+    uint32_t ph = (uint32_t)((g / nst) & 1);
+    const int64_t Mg = M > g ? (M - 1 - g) / NG + 1 : 0;
+    float2 h[kCPT][VP];  // h of the second pass's token, less the warp's mean
+    uint4 dxr[kCPT];
+    float wm = 0.0f;
+    for (int64_t i = 0; i <= Mg; ++i) {
+        float2 h1[kCPT][VP];
+        uint4 dx1[kCPT];
+        float wm1 = 0.0f;
+        if (i < Mg) {
+            // ---- first pass of token i ----
+            mbar_wait_bounded(&full[slot], ph, abort_flag, fault, FAULT_WAIT_FULL);
+            const unsigned char *st = smem + (int64_t)slot * sh.stage_bytes;
+            const float *at = wts + ws * kMaxStreams;
 #pragma unroll
             for (int u = 0; u < kCPT; ++u) {
                 const int k = k0 + u * kstep;
                 if (k < d) {
-                    float2 h[VP], dx[VP], gv[VP];
-                    load_f32(hr + k, h);
-                    load_f32(sg + k, gv);
-                    ck_widen(*reinterpret_cast<const uint4 *>(st + o_dx + k * (int)sizeof(S)), dx);
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) {
-                        const float2 c = fadd2_rn(h[e], nm), w = fmul2_rn(dx[e], gv[e]);
-                        s0 = fadd2_rn(s0, c);
-                        s1 = ffma2_rn(c, c, s1);
-                        s2 = fadd2_rn(s2, w);
-                        s3 = ffma2_rn(w, c, s3);
-                    }
-                }
-            }
-            const float v[4] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, s3.x + s3.y};
-            bw_warp_sums_to<4>(v, r4 + gw * 4, lane);
-        }
-        group_sync(1 + g, GT);
-        float4 tot = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < GW; ++w) {
-            const float4 f = *reinterpret_cast<const float4 *>(r4 + w * 4);
-            tot.x += f.x; tot.y += f.y; tot.z += f.z; tot.w += f.w;
-        }
-        const float off = tot.x * inv_d;  // what the mean lacks
-        const float var = fmaxf(__fmaf_rn(-off, off, tot.y * inv_d), 0.0f);
-        const float rs = tot.y == tot.y ? __frsqrt_rn(var + p.eps) : tot.y;  // fmaxf drops a NaN
-        const float c1 = tot.z * inv_d, c2 = rs * (tot.w - off * tot.z) * inv_d;
-        const float2 no = make_float2(-off, -off), r2 = make_float2(rs, rs);
-        const float2 n1 = make_float2(-c1, -c1), n2 = make_float2(-c2, -c2);
-
-        // the gradients
-        float dacc[N];
-#pragma unroll
-        for (int x = 0; x < N; ++x) dacc[x] = 0.0f;
-        S *DHt = DH + t * N * d;
-#pragma unroll
-        for (int u = 0; u < kCPT; ++u) {
-            const int k = k0 + u * kstep;
-            if (k < d) {
-                float2 z[VP], dx[VP], dh[VP];
-                load_f32(hr + k, z);
-                load_f32(sg + k, dh);
-                ck_widen(*reinterpret_cast<const uint4 *>(st + o_dx + k * (int)sizeof(S)), dx);
-#pragma unroll
-                for (int e = 0; e < VP; ++e) {
-                    z[e] = fmul2_rn(fadd2_rn(fadd2_rn(z[e], nm), no), r2);
-                    ag[u][e] = ffma2_rn(dx[e], z[e], ag[u][e]);
-                    ab[u][e] = fadd2_rn(dx[e], ab[u][e]);
-                    dh[e] = fmul2_rn(ffma2_rn(n2, z[e], fadd2_rn(fmul2_rn(dx[e], dh[e]), n1)), r2);
-                }
-#pragma unroll
-                for (int x = 0; x < N; ++x) {
-                    float2 o[VP];
-                    const float2 ax = make_float2(at[x], at[x]);
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) o[e] = fmul2_rn(ax, dh[e]);
-                    if (bp.da) {
+                    for (int x = 0; x < N; ++x) {
                         float2 v[VP];
                         load_row(st, x, k, v);
-                        float2 q = fmul2_rn(dh[0], v[0]);
+                        const float2 ax = make_float2(at[x], at[x]);
 #pragma unroll
-                        for (int e = 1; e < VP; ++e) q = ffma2_rn(dh[e], v[e], q);
-                        dacc[x] += q.x + q.y;
+                        for (int e = 0; e < VP; ++e)
+                            h1[u][e] = x == 0 ? fmul2_rn(ax, v[e]) : ffma2_rn(ax, v[e], h1[u][e]);
                     }
-                    __stcs(reinterpret_cast<uint4 *>(DHt + x * d + k), ck_narrow(o));
+                    dx1[u] = *reinterpret_cast<const uint4 *>(st + o_dx + k * (int)sizeof(S));
+                    float2 z = h1[u][0];
+#pragma unroll
+                    for (int e = 1; e < VP; ++e) z = fadd2_rn(z, h1[u][e]);
+                    wm1 += z.x + z.y;
                 }
             }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) wm1 += __shfl_xor_sync(0xffffffffu, wm1, o);
+            wm1 *= inv_n;
+            float2 q[3];
+#pragma unroll
+            for (int x = 0; x < 3; ++x) q[x] = make_float2(0.0f, 0.0f);
+            const float2 nm = make_float2(-wm1, -wm1);
+#pragma unroll
+            for (int u = 0; u < kCPT; ++u) {
+                const int k = k0 + u * kstep;
+                if (k < d) {
+                    float2 gv[VP], dx[VP];
+                    load_gains(k, gv);
+                    ck_widen(dx1[u], dx);
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) {
+                        h1[u][e] = fadd2_rn(h1[u][e], nm);
+                        const float2 w = fmul2_rn(dx[e], gv[e]);
+                        q[0] = ffma2_rn(h1[u][e], h1[u][e], q[0]);
+                        q[1] = fadd2_rn(q[1], w);
+                        q[2] = ffma2_rn(w, h1[u][e], q[2]);
+                    }
+                }
+            }
+            const float v[3] = {q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y};
+            float *rq = rg + (int)(i & 1) * 4 * 32 + gw;
+            warp_sums_put<3>(v, lane, [&](int x, float sx) { rq[x * 32] = sx; });
+            if (lane == 0) rq[3 * 32] = wm1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sums[g * 2 + (int)(i & 1)]);
+            for (slot += NG; slot >= nst; slot -= nst) ph ^= 1u;
+            for (ws += NG; ws >= sh.nw; ws -= sh.nw) {}
         }
-        if (bp.da) bw_warp_sums_to<N>(dacc, dr + gw * N, lane);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
-        t_prev = t;
+        if (i > 0) {
+            // ---- second pass of token i - 1 ----
+            const int par = (int)((i - 1) & 1);
+            mbar_wait_bounded(&stats[g * 2 + par], (uint32_t)(((i - 1) >> 1) & 1), abort_flag, fault,
+                              FAULT_WAIT_REDUCE);
+            const unsigned char *st = smem + (int64_t)slot0 * sh.stage_bytes;
+            const float *at = wts + ws0 * kMaxStreams;
+            const float4 so = *reinterpret_cast<const float4 *>(rg + kStat + par * 8);
+            const float k2 = rg[kStat + par * 8 + 4], own = (wm - so.x) - so.y;  // the warp's mean less the token's
+            const float2 nz = make_float2(own, own), r2 = make_float2(so.z, so.z);
+            const float2 n1 = make_float2(so.w, so.w), n2 = make_float2(k2, k2);
+            S *DHt = DH + (blockIdx.x + (g + (i - 1) * NG) * G) * N * d;
+            float dacc[N];
+#pragma unroll
+            for (int x = 0; x < N; ++x) dacc[x] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < kCPT; ++u) {
+                const int k = k0 + u * kstep;
+                if (k < d) {
+                    float2 dx[VP], dh[VP];
+                    load_gains(k, dh);
+                    ck_widen(dxr[u], dx);
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) {
+                        const float2 z = fmul2_rn(fadd2_rn(h[u][e], nz), r2);
+                        ag[u][e] = ffma2_rn(dx[e], z, ag[u][e]);
+                        ab[u][e] = fadd2_rn(dx[e], ab[u][e]);
+                        dh[e] = ffma2_rn(r2, fmul2_rn(dx[e], dh[e]), ffma2_rn(n2, z, n1));
+                    }
+#pragma unroll
+                    for (int x = 0; x < N; ++x) {
+                        float2 o[VP];
+                        const float2 ax = make_float2(at[x], at[x]);
+#pragma unroll
+                        for (int e = 0; e < VP; ++e) o[e] = fmul2_rn(ax, dh[e]);
+                        if (bp.da) {
+                            float2 v[VP];
+                            load_row(st, x, k, v);
+                            float2 q = fmul2_rn(dh[0], v[0]);
+#pragma unroll
+                            for (int e = 1; e < VP; ++e) q = ffma2_rn(dh[e], v[e], q);
+                            dacc[x] += q.x + q.y;
+                        }
+                        __stcs(reinterpret_cast<uint4 *>(DHt + x * d + k), ck_narrow(o));
+                    }
+                }
+            }
+            if (bp.da) {
+                float *dr = rg + kDa + par * N * 32 + gw;
+                warp_sums_put<N>(dacc, lane, [&](int x, float sx) { dr[x * 32] = sx; });
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot0]);
+            for (slot0 += NG; slot0 >= nst; slot0 -= nst) {}
+            for (ws0 += NG; ws0 >= sh.nw; ws0 -= sh.nw) {}
+        }
+#pragma unroll
+        for (int u = 0; u < kCPT; ++u) {
+#pragma unroll
+            for (int e = 0; e < VP; ++e) h[u][e] = h1[u][e];
+            dxr[u] = dx1[u];
+        }
+        wm = wm1;
     }
-    if (bp.da) {
-        group_sync(1 + g, GT);
-        if (gw == 0 && t_prev >= 0) write_da(t_prev);
-    }
+    if (lane == 0) mbar_arrive(&sums[g * 2 + (int)(Mg & 1)]);  // the last tokens' da sums are there
     if (bp.part) {
         // the groups' sums, added in group order over the stages (all consumed)
         float *acc = reinterpret_cast<float *>(smem);  // [2][d]
         for (int q = 0; q < NG; ++q) {
-            group_sync(15, NG * GT);
+            group_sync(1, NG * GT);
             if (q == g) {
 #pragma unroll
                 for (int u = 0; u < kCPT; ++u) {
@@ -655,10 +741,10 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
                 }
             }
         }
-        group_sync(15, NG * GT);
+        group_sync(1, NG * GT);
         float *row = bp.part + (int64_t)blockIdx.x * 2 * d;
-        for (int k = threadIdx.x * 4; k < 2 * d; k += NG * GT * 4)
-            *reinterpret_cast<float4 *>(row + k) = *reinterpret_cast<const float4 *>(acc + k);
+        for (int c = threadIdx.x * 4; c < 2 * d; c += NG * GT * 4)
+            *reinterpret_cast<float4 *>(row + c) = *reinterpret_cast<const float4 *>(acc + c);
     }
 }
 
@@ -745,8 +831,9 @@ struct LayerNorm {
         return HC_OK;
     }
     // The ring's geometry, or gw = 0 where it does not apply: a group's warps
-    // must cover the row, at least two stages (and the final sums) must fit,
-    // and a checkpoint's codes must start on 16 bytes.
+    // must cover the row, two stages a group and one more
+    // must fit (a group holds the tokens of both passes), and a checkpoint's
+    // codes must start on 16 bytes.
     static LnRingShape ring(int64_t d, bool packed, int64_t &smem) {
         LnRingShape sh{};
         const int64_t nvec = d / V, gw = (nvec + 32 * kCPT - 1) / (32 * kCPT);
@@ -754,12 +841,13 @@ struct LayerNorm {
         const int64_t stage = N * (packed ? d + ck_scale_stride(d) : d * (int64_t)sizeof(S)) + d * (int64_t)sizeof(S);
         for (int64_t ng = kRingWarps / gw; ng >= 1; --ng) {
             int64_t nst = (kSmemLimitLogits - ln_ring_fixed_bytes(N, d, (int)ng, 0)) / (stage + kMaxStreams * 4 + 16);
-            if (nst < ng + 1 && !(ng == 1 && nst >= 2)) continue;
-            if (nst > 2 * ng + 2) nst = 2 * ng + 2;
+            if (nst < 2 * ng + 1) continue;
+            if (nst > 3 * ng + 3) nst = 3 * ng + 3;
             if (nst * stage < 8 * d) continue;
             sh.gw = (int)gw;
             sh.ng = (int)ng;
             sh.nst = (int)nst;
+            sh.nw = (int)(nst + 2 * ng + 2);
             sh.stage_bytes = (int)stage;
             smem = nst * stage + ln_ring_fixed_bytes(N, d, (int)ng, (int)nst);
             break;
@@ -801,7 +889,7 @@ struct LayerNorm {
                     return set_error(HC_ERR_CUDA, "layer norm smem attribute: %s", cudaGetErrorString(e));
                 configured[ctx.device].store((int)smem);
             }
-            kern<<<(unsigned)g, 32 * (1 + sh.ng * sh.gw), (size_t)smem, st>>>(bp, sh, ctx.fault);
+            kern<<<(unsigned)g, 32 * (2 + sh.ng * sh.gw), (size_t)smem, st>>>(bp, sh, ctx.fault);
         } else {
             hc_layernorm_bwd_kernel<N, S, PACKED><<<(unsigned)g, threads(bp.f.d), (size_t)bp.f.d * 4, st>>>(bp);
         }
