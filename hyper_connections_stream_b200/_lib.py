@@ -615,8 +615,9 @@ class Checkpoint(NamedTuple):
 
 
 def checkpoint_scale_stride(d: int) -> int:
-    """Scale bytes a row of d values takes: one per 32 values, padded to 16."""
-    return int(lib().hc_checkpoint_scale_stride(int(d)))
+    """Scale bytes a row of d values takes: one per 32 values, padded to 16
+    (hc_checkpoint_scale_stride)."""
+    return (d + 511) // 512 * 16 if d > 0 else 0
 
 
 def checkpoint_empty(shape, device) -> Checkpoint:
@@ -645,10 +646,29 @@ def _rows(shape) -> int:
     return r
 
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+def _same_device(ref, *tensors):
+    """The tensors' device index; None entries are skipped."""
+    dev = ref.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, not on {ref.device}")
+    return dev
+
+
+def _call(dev, fn, *args):
+    """Call an entry point on dev's current stream, with dev current (the
+    library launches on the current device)."""
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != HC_OK:
+        raise HCError(st, lib().hc_last_error().decode())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def checkpoint_pack(x, *, out: Checkpoint | None = None) -> Checkpoint:
@@ -660,10 +680,9 @@ def checkpoint_pack(x, *, out: Checkpoint | None = None) -> Checkpoint:
         raise ValueError("x must be [..., d] float32 or bfloat16")
     out = checkpoint_empty(x.shape, x.device) if out is None else out
     _need_checkpoint("out", out, x.shape)
-    _same_device(x, out=out.codes, out_scales=out.scales)
-    with torch.cuda.device(x.device):
-        _check(lib().hc_checkpoint_pack(_ptr(x), _DT[x.dtype], _rows(x.shape), x.shape[-1], _ptr(out.codes),
-                                        _ptr(out.scales), _stream(x.device)))
+    dev = _same_device(x, out.codes, out.scales)
+    _call(dev, lib().hc_checkpoint_pack, x.data_ptr(), _DT[x.dtype], _rows(x.shape), x.shape[-1],
+          out.codes.data_ptr(), out.scales.data_ptr())
     return out
 
 
@@ -675,10 +694,9 @@ def checkpoint_unpack(c: Checkpoint, dtype=torch.bfloat16, *, out=None):
     shape = c.codes.shape
     out = torch.empty(shape, dtype=dtype, device=c.codes.device) if out is None else out
     _need_out("out", out, shape, dtype)
-    _same_device(c.codes, scales=c.scales, out=out)
-    with torch.cuda.device(out.device):
-        _check(lib().hc_checkpoint_unpack(_ptr(c.codes), _ptr(c.scales), _ptr(out), _DT[dtype], _rows(shape),
-                                          shape[-1], _stream(out.device)))
+    dev = _same_device(c.codes, c.scales, out)
+    _call(dev, lib().hc_checkpoint_unpack, c.codes.data_ptr(), c.scales.data_ptr(), out.data_ptr(), _DT[dtype],
+          _rows(shape), shape[-1])
     return out
 
 
@@ -707,13 +725,11 @@ def write_then_read_checkpoint(H, y, A, b, a_next, g_next=None, *, eps: float = 
     y_ckpt = checkpoint_empty((T, d), H.device) if y_ckpt is None else y_ckpt
     _need_checkpoint("H_ckpt", H_ckpt, (T, n, d))
     _need_checkpoint("y_ckpt", y_ckpt, (T, d))
-    _same_device(H, y=y, A=A, b=b, a_next=a_next, g_next=g_next, out=out, x_next=x_next, H_ckpt=H_ckpt.codes,
-                 H_ckpt_scales=H_ckpt.scales, y_ckpt=y_ckpt.codes, y_ckpt_scales=y_ckpt.scales)
-    with torch.cuda.device(H.device):
-        _check(lib().hc_write_then_read_checkpoint(
-            _ptr(H), _ptr(y), _ptr(out), _ptr(x_next), _DT[H.dtype], T, n, d, int(mix), _ptr(A), A_s, int(K),
-            _ptr(b), b_s, int(read), _ptr(a_next), a_s, _ptr(g_next), float(eps), _ptr(H_ckpt.codes),
-            _ptr(H_ckpt.scales), _ptr(y_ckpt.codes), _ptr(y_ckpt.scales), _stream(H.device)))
+    dev = _same_device(H, y, A, b, a_next, g_next, out, x_next, *H_ckpt, *y_ckpt)
+    _call(dev, lib().hc_write_then_read_checkpoint, H.data_ptr(), y.data_ptr(), out.data_ptr(), x_next.data_ptr(),
+          _DT[H.dtype], T, n, d, int(mix), A.data_ptr(), A_s, int(K), b.data_ptr(), b_s, int(read),
+          a_next.data_ptr(), a_s, _addr(g_next), float(eps), H_ckpt.codes.data_ptr(), H_ckpt.scales.data_ptr(),
+          y_ckpt.codes.data_ptr(), y_ckpt.scales.data_ptr())
     return out, x_next, H_ckpt, y_ckpt
 
 
@@ -740,30 +756,35 @@ def write_then_read_backward_checkpoint(H_ckpt: Checkpoint, y_ckpt: Checkpoint, 
     b_s = _tok_param("b", b, T, (n,))
     a_s = _tok_param("a", a, T, (n,))
     _need_gain("g", g, d)
-    dev = dx.device
-    _same_device(dx, H_ckpt=H_ckpt.codes, H_ckpt_scales=H_ckpt.scales, y_ckpt=y_ckpt.codes,
-                 y_ckpt_scales=y_ckpt.scales, A=A, b=b, a=a, g=g, dHout=dHout, workspace=workspace)
-    out = dict(dH=torch.empty((T, n, d), dtype=dx.dtype, device=dev), dy=torch.empty_like(dx),
-               dA=torch.empty((T, n, n), dtype=torch.float32, device=dev),
-               db=torch.empty((T, n), dtype=torch.float32, device=dev),
-               da=torch.empty((T, n), dtype=torch.float32, device=dev),
-               dg=torch.empty((d,), dtype=torch.float32, device=dev) if (g is not None and want_dg)
-               else None)
-    with torch.cuda.device(dev):
-        ws_bytes = 0
-        if out["dg"] is not None:
-            if workspace is None:
-                need = int(lib().hc_write_then_read_backward_checkpoint_workspace_bytes(_DT[dx.dtype], T, n, d))
-                workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
-            _need_cuda("workspace", workspace, torch.uint8)
-            ws_bytes = workspace.numel()
-        _check(lib().hc_write_then_read_backward_checkpoint(
-            _ptr(H_ckpt.codes), _ptr(H_ckpt.scales), _ptr(y_ckpt.codes), _ptr(y_ckpt.scales), _DT[dx.dtype],
-            T, n, d, int(mix), _ptr(A), A_s, int(K), _ptr(b), b_s, int(read), _ptr(a), a_s, _ptr(g), float(eps),
-            _ptr(dHout), _ptr(dx), _ptr(out["dH"]), _ptr(out["dy"]), _ptr(out["dA"]), _ptr(out["db"]),
-            _ptr(out["da"]), _ptr(out["dg"]), _ptr(workspace) if out["dg"] is not None else None, ws_bytes,
-            _stream(dev)))
+    dev = _same_device(dx, *H_ckpt, *y_ckpt, A, b, a, g, dHout, workspace)
+    empty = dx.new_empty
+    out = dict(dH=empty((T, n, d)), dy=empty((T, d)), dA=empty((T, n, n), dtype=torch.float32),
+               db=empty((T, n), dtype=torch.float32), da=empty((T, n), dtype=torch.float32),
+               dg=empty((d,), dtype=torch.float32) if (g is not None and want_dg) else None)
+    ws_bytes = 0
+    if out["dg"] is None:
+        workspace = None
+    else:
+        if workspace is None:
+            workspace = empty((_workspace_bytes("hc_write_then_read_backward_checkpoint_workspace_bytes", dev,
+                                                dx.dtype, T, n, d),), dtype=torch.uint8)
+        _need_cuda("workspace", workspace, torch.uint8)
+        ws_bytes = workspace.numel()
+    _call(dev, lib().hc_write_then_read_backward_checkpoint, H_ckpt.codes.data_ptr(), H_ckpt.scales.data_ptr(),
+          y_ckpt.codes.data_ptr(), y_ckpt.scales.data_ptr(), _DT[dx.dtype], T, n, d, int(mix), A.data_ptr(), A_s,
+          int(K), b.data_ptr(), b_s, int(read), a.data_ptr(), a_s, _addr(g), float(eps), _addr(dHout),
+          dx.data_ptr(), out["dH"].data_ptr(), out["dy"].data_ptr(), out["dA"].data_ptr(), out["db"].data_ptr(),
+          out["da"].data_ptr(), _addr(out["dg"]), _addr(workspace), ws_bytes)
     return out
+
+
+def _workspace_bytes(query, dev, dtype, T, n, d):
+    """The library's answer for dev, at least 16 bytes."""
+    fn = getattr(lib(), query)
+    if torch.cuda.current_device() == dev:
+        return max(16, fn(_DT[dtype], T, n, d))
+    with torch.cuda.device(dev):
+        return max(16, fn(_DT[dtype], T, n, d))
 
 
 def _read_param(a, T, n):
@@ -786,10 +807,9 @@ def read_layernorm(H, a, g=None, beta=None, *, eps: float = 1e-6, read: int = RE
     _need_gain("beta", beta, d)
     x = torch.empty((T, d), dtype=H.dtype, device=H.device) if x is None else x
     _need_out("x", x, (T, d), H.dtype)
-    _same_device(H, a=a, g=g, beta=beta, x=x)
-    with torch.cuda.device(H.device):
-        _check(lib().hc_read_layernorm(_ptr(H), _ptr(x), _DT[H.dtype], T, n, d, int(read), _ptr(a), a_s, _ptr(g),
-                                       _ptr(beta), float(eps), _stream(H.device)))
+    dev = _same_device(H, a, g, beta, x)
+    _call(dev, lib().hc_read_layernorm, H.data_ptr(), x.data_ptr(), _DT[H.dtype], T, n, d, int(read), _addr(a), a_s,
+          _addr(g), _addr(beta), float(eps))
     return x
 
 
@@ -817,22 +837,21 @@ def read_layernorm_backward(H, a, g, dx, *, eps: float = 1e-6, read: int = READ_
         raise ValueError("dx must be [T, d]")
     a_s = _read_param(a, T, n)
     _need_gain("g", g, d)
-    dev = dx.device
-    _same_device(dx, H=rows, H_scales=scales, a=a, g=g, workspace=workspace)
-    f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)
-    out = dict(dH=torch.empty((T, n, d), dtype=dx.dtype, device=dev), da=f32(T, n) if a is not None else None,
-               dg=f32(d) if (g is not None and want_dg) else None, dbeta=f32(d) if want_dbeta else None)
-    with torch.cuda.device(dev):
-        ws_bytes = 0
-        sums = out["dg"] is not None or out["dbeta"] is not None
-        if sums:
-            if workspace is None:
-                need = int(lib().hc_read_layernorm_backward_workspace_bytes(_DT[dx.dtype], T, n, d))
-                workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
-            _need_cuda("workspace", workspace, torch.uint8)
-            ws_bytes = workspace.numel()
-        _check(lib().hc_read_layernorm_backward(
-            _ptr(rows), _ptr(scales), _DT[dx.dtype], T, n, d, int(read), _ptr(a), a_s, _ptr(g), float(eps),
-            _ptr(dx), _ptr(out["dH"]), _ptr(out["da"]), _ptr(out["dg"]), _ptr(out["dbeta"]),
-            _ptr(workspace) if sums else None, ws_bytes, _stream(dev)))
+    dev = _same_device(dx, rows, scales, a, g, workspace)
+    empty = dx.new_empty
+    out = dict(dH=empty((T, n, d)), da=empty((T, n), dtype=torch.float32) if a is not None else None,
+               dg=empty((d,), dtype=torch.float32) if (g is not None and want_dg) else None,
+               dbeta=empty((d,), dtype=torch.float32) if want_dbeta else None)
+    ws_bytes = 0
+    if out["dg"] is None and out["dbeta"] is None:
+        workspace = None
+    else:
+        if workspace is None:
+            workspace = empty((_workspace_bytes("hc_read_layernorm_backward_workspace_bytes", dev, dx.dtype, T, n,
+                                                d),), dtype=torch.uint8)
+        _need_cuda("workspace", workspace, torch.uint8)
+        ws_bytes = workspace.numel()
+    _call(dev, lib().hc_read_layernorm_backward, rows.data_ptr(), _addr(scales), _DT[dx.dtype], T, n, d, int(read),
+          _addr(a), a_s, _addr(g), float(eps), dx.data_ptr(), out["dH"].data_ptr(), _addr(out["da"]),
+          _addr(out["dg"]), _addr(out["dbeta"]), _addr(workspace), ws_bytes)
     return out

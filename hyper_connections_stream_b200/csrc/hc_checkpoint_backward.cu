@@ -20,6 +20,8 @@
 // slices. dH' and dx are read again from L2 in the second pass, h is parked in
 // shared memory (fp32; rebuilt from the checkpoint where a row does not fit).
 // The gain gradient accumulates in the CTA's workspace row.
+#include <atomic>
+
 #include "hc_checkpoint.cuh"
 #include "hc_launch.h"
 #include "hc_token_sums.cuh"
@@ -282,22 +284,35 @@ struct CkBw {
             if (nvec % c == 0) return (int)c;
         return (int)nt;
     }
+    // Shared memory opted in once per device.
     template <bool PARK>
-    static hc_status occupancy(int NT, size_t dyn, int &per_sm) {
-        auto kern = hc_ck_bwd_kernel<N, S, PARK>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, NT, dyn);
+    static hc_status configure(const LaunchCtx &ctx) {
+        static std::atomic<bool> done[64];
+        if (ctx.device < 0 || ctx.device >= 64)
+            return set_error(HC_ERR_UNSUPPORTED, "device ordinal %d >= 64", ctx.device);
+        if (done[ctx.device].load()) return HC_OK;
+        const cudaError_t e = cudaFuncSetAttribute(hc_ck_bwd_kernel<N, S, PARK>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
         if (e != cudaSuccess)
-            return set_error(HC_ERR_CUDA, "checkpoint backward occupancy: %s", cudaGetErrorString(e));
+            return set_error(HC_ERR_CUDA, "checkpoint backward smem attribute: %s", cudaGetErrorString(e));
+        done[ctx.device].store(true);
         return HC_OK;
     }
     static hc_status grid(int64_t T, int64_t d, const LaunchCtx &ctx, int64_t &grid) {
+        const bool park = parked(d);
+        const hc_status s = park ? configure<true>(ctx) : configure<false>(ctx);
+        if (s != HC_OK) return s;
+        grid = T;
+        if (T <= ctx.sms) return HC_OK;
         int per_sm = 0;
         const int NT = threads(d);
-        const hc_status s = parked(d) ? occupancy<true>(NT, (size_t)d * 4, per_sm) : occupancy<false>(NT, 0, per_sm);
-        if (s != HC_OK) return s;
-        grid = (int64_t)ctx.sms * (per_sm < 1 ? 1 : per_sm);
-        if (grid > T) grid = T;
+        const cudaError_t e =
+            park ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, hc_ck_bwd_kernel<N, S, true>, NT, (size_t)d * 4)
+                 : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, hc_ck_bwd_kernel<N, S, false>, NT, 0);
+        if (e != cudaSuccess)
+            return set_error(HC_ERR_CUDA, "checkpoint backward occupancy: %s", cudaGetErrorString(e));
+        const int64_t most = (int64_t)ctx.sms * (per_sm < 1 ? 1 : per_sm);
+        if (grid > most) grid = most;
         return HC_OK;
     }
     static hc_status launch(const BackwardArgs &a, const uint8_t *sH, const uint8_t *sy, int64_t g,

@@ -780,11 +780,15 @@ struct LayerNorm {
     template <int CPT>
     static hc_status forward_cpt(const LayerNormArgs &a, int NT, const LaunchCtx &ctx, cudaStream_t st) {
         auto kern = hc_layernorm_kernel<N, S, CPT>;
-        int per_sm = 0;
-        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, NT, 0);
-        if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "layer norm occupancy: %s", cudaGetErrorString(e));
-        int64_t grid = (int64_t)ctx.sms * (per_sm < 1 ? 1 : per_sm);
-        if (grid > a.f.T) grid = a.f.T;
+        int64_t grid = a.f.T;
+        cudaError_t e;
+        if (grid > ctx.sms) {
+            int per_sm = 0;
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, NT, 0);
+            if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "layer norm occupancy: %s", cudaGetErrorString(e));
+            const int64_t most = (int64_t)ctx.sms * (per_sm < 1 ? 1 : per_sm);
+            if (grid > most) grid = most;
+        }
         kern<<<(unsigned)grid, NT, 0, st>>>(a.f, a.beta);
         e = cudaGetLastError();
         if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "hc_layernorm_kernel launch: %s", cudaGetErrorString(e));

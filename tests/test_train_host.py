@@ -169,7 +169,7 @@ def test_scale_stride():
     from hyper_connections_stream_b200 import _lib
     L = _lib.lib()
     for d, want in ((0, 0), (-3, 0), (4, 16), (32, 16), (512, 16), (516, 32), (7168, 224), (7200, 240), (32768, 1024)):
-        assert L.hc_checkpoint_scale_stride(d) == want, d
+        assert L.hc_checkpoint_scale_stride(d) == want == _lib.checkpoint_scale_stride(d), d
 
 
 def test_binding_refuses_host_tensors_and_foreign_types():
