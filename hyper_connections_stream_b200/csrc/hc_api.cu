@@ -881,12 +881,9 @@ hc_status hc_write_then_read_checkpoint(const void *H, const void *y, void *Hout
     p.a = a_next; p.a_s = a_tok_stride; p.g = g_next; p.eps = eps;
     p.K = K; p.mix_logits = mm == HC_MIX_SINKHORN_LOGITS;
     p.read_logits = rm == HC_READ_SOFTMAX_LOGITS;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    hc::LaunchCtx ctx{};
-    HC_TRY(launch_ctx(ctx));
-    HC_TRY(hc::launch_checkpoint_pack(H, dt, H_codes, H_scales, T * n, d, ctx, st));
-    HC_TRY(hc::launch_checkpoint_pack(y, dt, y_codes, y_scales, T, d, ctx, st));
-    return dispatch<hc::KIND_FUSED>(dt, n, p, st);
+    p.qH = H_codes; p.sH = H_scales; p.qy = y_codes; p.sy = y_scales;
+    p.ns = ns;
+    return dispatch<hc::KIND_SAVE>(dt, n, p, static_cast<cudaStream_t>(stream));
 }
 
 size_t hc_write_then_read_backward_checkpoint_workspace_bytes(hc_dtype dt, int64_t T, int n, int64_t d) {

@@ -112,6 +112,21 @@ __device__ __forceinline__ void ck_store(uint8_t *p, const uint32_t (&q)[V / 4])
     else __stcs(reinterpret_cast<unsigned int *>(p), q[0]);
 }
 
+// Keep VP pairs at column k of a row (codes at q, exponents at s), called by
+// the whole warp; lanes past the row's end pass in = false.
+template <int VP>
+__device__ __forceinline__ void ck_keep(const float2 (&v)[VP], bool in, uint8_t *q, uint8_t *s, int64_t k, int lane) {
+    float2 w[VP];
+#pragma unroll
+    for (int p = 0; p < VP; ++p) w[p] = in ? v[p] : make_float2(0.0f, 0.0f);
+    uint32_t c[(VP + 1) / 2], e;
+    ck_encode<VP>(w, c, e);
+    if (in) {
+        ck_store<2 * VP>(q + k, c);
+        if (lane % (kCkBlock / (2 * VP)) == 0) s[k / kCkBlock] = (uint8_t)e;
+    }
+}
+
 // Storage values as fp32 pairs: 16 bytes (V elements) to and from global memory.
 __device__ __forceinline__ void ck_widen(uint4 q, float2 (&v)[4]) {
     widen_bf16x2(q.x, v[0].x, v[0].y);

@@ -20,7 +20,8 @@ constexpr int kStreamMaxThreads = 512;
 // also produces layer 0's block input from them, COLLAPSE mixes the n
 // streams into one row (no normalisation). REDUCE is FUSED with y the sum of
 // R ranks' partial block outputs (the tensor-parallel all-reduce folded into
-// the write; pipelined family only).
+// the write; pipelined family only). SAVE is FUSED that also keeps an 8-bit
+// checkpoint of the H and y it reads (hc_checkpoint.cuh).
 enum Kind {
     KIND_READ = 0,
     KIND_WRITE = 1,
@@ -28,12 +29,14 @@ enum Kind {
     KIND_EXPAND = 3,
     KIND_EXPAND_READ = 4,
     KIND_COLLAPSE = 5,
-    KIND_REDUCE = 6
+    KIND_REDUCE = 6,
+    KIND_SAVE = 7
 };
 
 // Kinds that normalise a mixed row (a CTA-wide statistic per token).
 __host__ __device__ constexpr bool kind_normalises(int kind) {
-    return kind == KIND_READ || kind == KIND_FUSED || kind == KIND_EXPAND_READ || kind == KIND_REDUCE;
+    return kind == KIND_READ || kind == KIND_FUSED || kind == KIND_EXPAND_READ || kind == KIND_REDUCE ||
+           kind == KIND_SAVE;
 }
 
 // ---------------------------------------------------------------------------
@@ -319,6 +322,8 @@ struct StepParams {
     int K;
     int mix_logits;   // 1: A holds Sinkhorn logits
     int read_logits;  // 1: a holds softmax logits
+    uint8_t *qH, *sH, *qy, *sy;  // KIND_SAVE: codes and scales of H and y
+    int64_t ns;                  // KIND_SAVE: scale bytes per row
 };
 
 // Fill the shared-memory parameter block for TB tokens of this CTA's token

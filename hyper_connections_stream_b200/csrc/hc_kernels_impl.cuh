@@ -100,7 +100,7 @@ bool pipe_shape(const StepParams &p, int rows, PipeShape &sh, int &smem) {
     if (per_group < 2) return false;
     if (per_group > kMaxStages / kPipeGroups) per_group = kMaxStages / kPipeGroups;
     const int64_t cap = KIND == KIND_WRITE ? HC_PIPE_SG_WRITE
-                        : KIND == KIND_FUSED ? HC_PIPE_SG_FUSED
+                        : KIND == KIND_FUSED || KIND == KIND_SAVE ? HC_PIPE_SG_FUSED
                         : KIND == KIND_REDUCE ? HC_PIPE_SG_REDUCE : HC_PIPE_SG_READ;
     if (per_group > cap) per_group = cap;
     if (per_group < 1) per_group = 1;
@@ -187,7 +187,7 @@ int step_path_n(const StepParams &p, const LaunchCtx &ctx, bool &pipe_ok, bool &
     bool small = p.T * (int64_t)N * p.d * (int64_t)sizeof(S) * 2 < (int64_t(64) << 20);
     if constexpr (KIND == KIND_READ) small = true;
     if constexpr (KIND == KIND_WRITE && N <= 2) small = true;
-    if constexpr (KIND == KIND_FUSED) {
+    if constexpr (KIND == KIND_FUSED || KIND == KIND_SAVE) {
         constexpr int64_t tmin_n[9] = {0, 512, 512, 256, 256, 1024, 4096, 2048, 2048};
         constexpr int64_t ragged_x[9] = {0, int64_t(1) << 40, 64, 4, 4, 16, 4, 4, 4};
         // raggedness of the default width, which the thresholds were fitted on
@@ -220,7 +220,7 @@ hc_status launch_step_n(const StepParams &p, const LaunchCtx &ctx, cudaStream_t 
 
 template <int N, typename S, int KIND>
 hc_status launch_n(const StepParams &p, const LaunchCtx &ctx, cudaStream_t st) {
-    if constexpr (KIND >= KIND_EXPAND) {
+    if constexpr (KIND >= KIND_EXPAND && KIND != KIND_SAVE) {
         // the ends of a stack run once per pass: register-streaming family only
         if (kind_normalises(KIND) && p.d > (int64_t)kStreamMaxThreads * 8 * StorageTraits<S>::V)
             return set_error(HC_ERR_UNSUPPORTED, "d = %lld too large", (long long)p.d);

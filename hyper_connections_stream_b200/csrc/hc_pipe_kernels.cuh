@@ -31,6 +31,7 @@
 // code, stops issuing, drains the copies it issued and exits.
 #pragma once
 
+#include "hc_checkpoint.cuh"
 #include "hc_device.cuh"
 #include "hc_sync.cuh"
 
@@ -668,6 +669,12 @@ hc_pipe_kernel(StepParams p, PipeShape sh, int *fault, PipeReduce rd) {
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&gempty[cs]);  // stage data is in registers
+                if constexpr (KIND == KIND_SAVE) {  // the checkpoint of what the step reads
+#pragma unroll
+                    for (int ii = 0; ii < N; ++ii)
+                        ck_keep<VP>(h[ii], active, p.qH + (t * N + ii) * d, p.sH + (t * N + ii) * p.ns, k, lane);
+                    ck_keep<VP>(yv, active, p.qy + t * d, p.sy + t * p.ns, k, lane);
+                }
                 if (active) {
                     if constexpr (REDUCE) {
                         // one rounding to the storage dtype (what a stored y holds)

@@ -10,6 +10,7 @@
 // KIND_WRITE:  H, y -> H'                    (no reduction, no barrier per token)
 // KIND_READ:   H -> x = RMSNorm(a^T H) g
 // KIND_FUSED:  H, y -> H', x = RMSNorm(a^T H') g (H' not read back)
+// KIND_SAVE:   KIND_FUSED, and the 8-bit checkpoint of H and y
 // KIND_EXPAND:      e -> H' with every stream a copy of e (p.y holds e)
 // KIND_EXPAND_READ: e -> H' as above, x = RMSNorm(a^T H') g (H' not read back)
 // KIND_COLLAPSE:    H -> x = a^T H, stored without normalisation
@@ -18,6 +19,7 @@
 // shared-memory exchange per token), so each byte crosses HBM once.
 #pragma once
 
+#include "hc_checkpoint.cuh"
 #include "hc_device.cuh"
 
 namespace hc {
@@ -30,7 +32,8 @@ __global__ void __launch_bounds__(kStreamMaxThreads)
 hc_stream_kernel(StepParams p) {
     constexpr int V = StorageTraits<S>::V;
     constexpr int NN = N * N;
-    constexpr bool WRITE = KIND == KIND_WRITE || KIND == KIND_FUSED;  // A, b per token
+    constexpr bool SAVE = KIND == KIND_SAVE;
+    constexpr bool WRITE = KIND == KIND_WRITE || KIND == KIND_FUSED || SAVE;  // A, b per token
     constexpr bool READ = KIND != KIND_WRITE && KIND != KIND_EXPAND;  // a per token
     constexpr int TB_MAX = kPrepTokens;
 
@@ -125,6 +128,23 @@ hc_stream_kernel(StepParams p) {
 #pragma unroll
                 for (int u = 0; u < CPT; ++u) {
                     const int64_t c = tid + (int64_t)u * NT;
+                    [[maybe_unused]] float2 kept[SAVE ? N + 1 : 1][V / 2];
+                    if constexpr (SAVE) {  // loaded by the whole warp, which shares the blocks of 32
+                        const bool in = c < nvec;
+#pragma unroll
+                        for (int i = 0; i <= N; ++i) {
+                            const int64_t row = i < N ? t * N + i : t;
+                            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                            if (in) raw = __ldcs(reinterpret_cast<const uint4 *>((i < N ? H : Y) + row * p.d + c * V));
+                            ck_widen(raw, kept[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i <= N; ++i) {
+                            const int64_t row = i < N ? t * N + i : t;
+                            ck_keep<V / 2>(kept[i], in, (i < N ? p.qH : p.qy) + row * p.d,
+                                           (i < N ? p.sH : p.sy) + row * p.ns, c * V, tid & 31);
+                        }
+                    }
                     if (c < nvec) {
                         const int64_t k = c * V;
 #pragma unroll
@@ -140,12 +160,21 @@ hc_stream_kernel(StepParams p) {
 #pragma unroll
                                 for (int e = 0; e < V; ++e) hs[u][e] = __fmaf_rn(aj, ev[e], hs[u][e]);
                             }
-                        } else if constexpr (KIND == KIND_FUSED) {
+                        } else if constexpr (KIND == KIND_FUSED || SAVE) {
                             float h[N][V];
-#pragma unroll
-                            for (int i = 0; i < N; ++i) load_vec_cs(Ht + i * p.d + k, h[i]);
                             float yv[V];
-                            load_vec_cs(Y + t * p.d + k, yv);
+                            if constexpr (SAVE) {
+#pragma unroll
+                                for (int e = 0; e < V; ++e) {
+#pragma unroll
+                                    for (int i = 0; i < N; ++i) h[i][e] = e & 1 ? kept[i][e / 2].y : kept[i][e / 2].x;
+                                    yv[e] = e & 1 ? kept[N][e / 2].y : kept[N][e / 2].x;
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < N; ++i) load_vec_cs(Ht + i * p.d + k, h[i]);
+                                load_vec_cs(Y + t * p.d + k, yv);
+                            }
 #pragma unroll
                             for (int j = 0; j < N; ++j) {
                                 float acc[V], stored[V];
