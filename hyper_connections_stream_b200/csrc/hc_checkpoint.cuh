@@ -37,12 +37,10 @@ __device__ __forceinline__ float ck_scale(uint32_t e) { return __uint_as_float(e
 __device__ __forceinline__ float ck_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 
 // Two codes (element 0 in the low byte) of values already divided by the
-// scale. x * 0 + x is x for finite x and NaN for an infinity, which the
-// conversion's saturation would otherwise turn into 448.
+// scale; NaN becomes NaN, an infinity 448.
 __device__ __forceinline__ uint32_t ck_encode2(float2 x) {
-    const float2 z = ffma2_rn(x, make_float2(0.0f, 0.0f), x);
     uint16_t q;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(z.y), "f"(z.x));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(x.y), "f"(x.x));
     return q;
 }
 // The two values (before scaling) of the codes in the low 16 bits.
@@ -61,19 +59,24 @@ __device__ __forceinline__ uint32_t ck_finite_bits(float x) {
 // The codes of VP pairs of one thread. The 32 / (2 VP) neighbouring lanes that
 // share a block exchange their maxima, so all lanes of the warp call this
 // together (a lane past the row's end passes zeros); e receives the block's
-// biased exponent. Word w of q holds elements 4 w .. 4 w + 3.
+// biased exponent. Word w of q holds elements 4 w .. 4 w + 3. The floating
+// maximum passes over NaN; an infinity (or nothing but NaN) shows in it.
 template <int VP>
 __device__ __forceinline__ void ck_encode(const float2 (&v)[VP], uint32_t (&q)[(VP + 1) / 2], uint32_t &e) {
-    uint32_t m = 0;
+    float mf = fmaxf(fabsf(v[0].x), fabsf(v[0].y));
 #pragma unroll
-    for (int p = 0; p < VP; ++p) {
-        m = max(m, __float_as_uint(v[p].x) & 0x7fffffffu);
-        m = max(m, __float_as_uint(v[p].y) & 0x7fffffffu);
-    }
-    if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {  // rare: leave infinities and NaN out
+    for (int p = 1; p < VP; ++p) mf = fmaxf(mf, fmaxf(fabsf(v[p].x), fabsf(v[p].y)));
+    uint32_t m = __float_as_uint(mf) & 0x7fffffffu;
+    float2 w[VP];
+#pragma unroll
+    for (int p = 0; p < VP; ++p) w[p] = v[p];
+    if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {  // rare: infinities become NaN and leave the maximum
         m = 0;
 #pragma unroll
-        for (int p = 0; p < VP; ++p) m = max(m, max(ck_finite_bits(v[p].x), ck_finite_bits(v[p].y)));
+        for (int p = 0; p < VP; ++p) {
+            m = max(m, max(ck_finite_bits(v[p].x), ck_finite_bits(v[p].y)));
+            w[p] = ffma2_rn(v[p], make_float2(0.0f, 0.0f), v[p]);  // x * 0 + x: x, or NaN for an infinity
+        }
     }
 #pragma unroll
     for (int o = kCkBlock / (4 * VP); o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -82,8 +85,8 @@ __device__ __forceinline__ void ck_encode(const float2 (&v)[VP], uint32_t (&q)[(
     const float2 i2 = make_float2(inv, inv);
 #pragma unroll
     for (int p = 0; p < VP; p += 2) {
-        q[p / 2] = ck_encode2(fmul2_rn(v[p], i2));
-        if (p + 1 < VP) q[p / 2] |= ck_encode2(fmul2_rn(v[p + 1], i2)) << 16;
+        q[p / 2] = ck_encode2(fmul2_rn(w[p], i2));
+        if (p + 1 < VP) q[p / 2] |= ck_encode2(fmul2_rn(w[p + 1], i2)) << 16;
     }
 }
 
