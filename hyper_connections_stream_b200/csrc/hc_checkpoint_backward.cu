@@ -92,6 +92,11 @@ __device__ __forceinline__ void ck_write_params(const double *fin, const float *
     __syncwarp();
 }
 
+// Ask for `bytes` at p to be brought into L2 (both multiples of 16).
+__device__ __forceinline__ void prefetch_l2(const void *p, int64_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)bytes) : "memory");
+}
+
 template <int N, typename S, bool PARK>
 __global__ void __launch_bounds__(kThreads, (N <= 4 ? 2 : 1))
 hc_ck_bwd_kernel(CkBwParams bp) {
@@ -142,6 +147,17 @@ hc_ck_bwd_kernel(CkBwParams bp) {
             const int64_t t = first + (int64_t)tt * G;
             if (t >= p.T) break;  // uniform over the CTA
             const float *At = sA + tt * NN, *bt = sb + tt * N, *at = sa + tt * N, *ct = sc + tt * (N + 1);
+            // the next token's rows into L2 while this one is worked on: the
+            // first pass then waits for L2, not for DRAM
+            if (tid == 0 && t + G < p.T && d % 16 == 0) {
+                const int64_t u = t + G;
+                if (DHO) prefetch_l2(DHO + u * N * d, N * d * (int64_t)sizeof(S));
+                prefetch_l2(DX + u * d, d * (int64_t)sizeof(S));
+                prefetch_l2(QH + u * N * d, N * d);
+                prefetch_l2(QY + u * d, d);
+                prefetch_l2(bp.sH + u * N * bp.ns, N * bp.ns);
+                prefetch_l2(bp.sy + u * bp.ns, bp.ns);
+            }
 
             // the checkpoint's values of slice k: H rows, then y
             auto load_kept = [&](int64_t k, float2 (&hv)[N + 1][VP]) {
