@@ -113,7 +113,8 @@ hc_ck_bwd_kernel(CkBwParams bp) {
 
     const int tid = threadIdx.x, NT = blockDim.x, nwarps = NT >> 5;
     const int lane = tid & 31, warp = tid >> 5;
-    const int64_t d = p.d, nvec = d / V, G = gridDim.x;
+    const int64_t G = gridDim.x;
+    const int d = (int)p.d, ns = (int)bp.ns;  // columns and a token's rows fit 32 bits
     int TB = nwarps * Group<N>::TPW;
     TB = TB < kTB ? TB : kTB;
     const uint8_t *QH = static_cast<const uint8_t *>(p.H), *QY = static_cast<const uint8_t *>(p.y);
@@ -121,10 +122,10 @@ hc_ck_bwd_kernel(CkBwParams bp) {
     S *DH = static_cast<S *>(bp.dH), *DY = static_cast<S *>(bp.dy);
     float *sdg = bp.dg_part ? bp.dg_part + (int64_t)blockIdx.x * d : nullptr;
     if (sdg)
-        for (int64_t c = tid; c < nvec; c += NT) {
+        for (int k = tid * V; k < d; k += NT * V) {
 #pragma unroll
             for (int e = 0; e < V; e += 4)
-                *reinterpret_cast<float4 *>(sdg + c * V + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4 *>(sdg + k + e) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
 
     for (int64_t m0 = 0;; m0 += TB) {
@@ -159,16 +160,21 @@ hc_ck_bwd_kernel(CkBwParams bp) {
                 prefetch_l2(bp.sy + u * bp.ns, bp.ns);
             }
 
+            const uint8_t *QHt = QH + t * N * d, *QYt = QY + t * d;
+            const uint8_t *EHt = bp.sH + t * N * ns, *EYt = bp.sy + t * ns;
+            const S *DHOt = DHO ? DHO + t * N * d : nullptr, *DXt = DX + t * d;
+            S *DHt = DH + t * N * d, *DYt = DY + t * d;
+
             // the checkpoint's values of slice k: H rows, then y
-            auto load_kept = [&](int64_t k, float2 (&hv)[N + 1][VP]) {
+            auto load_kept = [&](int k, float2 (&hv)[N + 1][VP]) {
+                uint32_t q[N + 1][V / 4], e[N + 1];
 #pragma unroll
                 for (int i = 0; i <= N; ++i) {
-                    const int64_t row = i < N ? t * N + i : t;
-                    uint32_t q[V / 4];
-                    ck_load<V>((i < N ? QH : QY) + row * d + k, q);
-                    const uint32_t e = __ldg((i < N ? bp.sH : bp.sy) + row * bp.ns + k / kCkBlock);
-                    ck_decode<VP>(q, ck_scale(e), hv[i]);
+                    ck_load<V>(i < N ? QHt + (i * d + k) : QYt + k, q[i]);
+                    e[i] = __ldg(i < N ? EHt + (i * ns + k / kCkBlock) : EYt + k / kCkBlock);
                 }
+#pragma unroll
+                for (int i = 0; i <= N; ++i) ck_decode<VP>(q[i], ck_scale(e[i]), hv[i]);
             };
             auto mix_h = [&](const float2 (&hv)[N + 1][VP], float2 (&h)[VP]) {
 #pragma unroll
@@ -183,11 +189,10 @@ hc_ck_bwd_kernel(CkBwParams bp) {
             float acc[NV];
 #pragma unroll
             for (int v = 0; v < NV; ++v) acc[v] = 0.0f;
-            for (int64_t c = tid; c < nvec; c += NT) {
-                const int64_t k = c * V;
+            for (int k = tid * V; k < d; k += NT * V) {
                 float2 hv[N + 1][VP], h[VP], u[VP], gv[VP];
                 load_kept(k, hv);
-                ck_widen(__ldg(reinterpret_cast<const uint4 *>(DX + t * d + k)), u);
+                ck_widen(__ldg(reinterpret_cast<const uint4 *>(DXt + k)), u);
                 load_gain2<VP>(p.g, k, gv);
 #pragma unroll
                 for (int e = 0; e < VP; ++e) u[e] = fmul2_rn(u[e], gv[e]);
@@ -216,7 +221,7 @@ hc_ck_bwd_kernel(CkBwParams bp) {
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         float2 gr[VP];
-                        ck_widen(__ldg(reinterpret_cast<const uint4 *>(DHO + (t * N + j) * d + k)), gr);
+                        ck_widen(__ldg(reinterpret_cast<const uint4 *>(DHOt + (j * d + k))), gr);
 #pragma unroll
                         for (int i = 0; i < N; ++i) dot(hv[i], gr, acc[i * N + j]);
                         dot(hv[N], gr, acc[Q::B + j]);
@@ -231,10 +236,9 @@ hc_ck_bwd_kernel(CkBwParams bp) {
 
             // ---- pass 2: the gradients of H and y ----
             const float2 r2 = make_float2(stat[0], stat[0]), nq2 = make_float2(-stat[1], -stat[1]);
-            for (int64_t c = tid; c < nvec; c += NT) {
-                const int64_t k = c * V;
+            for (int k = tid * V; k < d; k += NT * V) {
                 float2 dx[VP], gv[VP], h[VP], dh[VP];
-                ck_widen(__ldcs(reinterpret_cast<const uint4 *>(DX + t * d + k)), dx);
+                ck_widen(__ldcs(reinterpret_cast<const uint4 *>(DXt + k)), dx);
                 load_gain2<VP>(p.g, k, gv);
                 if constexpr (PARK) {
 #pragma unroll
@@ -269,7 +273,7 @@ hc_ck_bwd_kernel(CkBwParams bp) {
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         float2 gr[VP];
-                        ck_widen(__ldcs(reinterpret_cast<const uint4 *>(DHO + (t * N + j) * d + k)), gr);
+                        ck_widen(__ldcs(reinterpret_cast<const uint4 *>(DHOt + (j * d + k))), gr);
 #pragma unroll
                         for (int i = 0; i <= N; ++i) {
                             const float w = i < N ? At[i * N + j] : bt[j];
@@ -280,8 +284,8 @@ hc_ck_bwd_kernel(CkBwParams bp) {
                 }
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    __stcs(reinterpret_cast<uint4 *>(DH + (t * N + i) * d + k), ck_narrow(o[i]));
-                __stcs(reinterpret_cast<uint4 *>(DY + t * d + k), ck_narrow(o[N]));
+                    __stcs(reinterpret_cast<uint4 *>(DHt + (i * d + k)), ck_narrow(o[i]));
+                __stcs(reinterpret_cast<uint4 *>(DYt + k), ck_narrow(o[N]));
             }
         }
     }

@@ -7,11 +7,10 @@
 // (then da through the read softmax). Bound by memory: n + 1 rows of d in or
 // out a token forward, 2 n + 1 backward, and few operations an element.
 //
-// Moments: every thread takes its first element of h as pivot p and sums
-// h - p and (h - p)^2 in fp32; the sums of h and h^2 (and of u h) follow in
-// fp64, where they are added over the CTA. One pass and one exchange, and a
-// mean much larger than the deviation costs no accuracy: the fp32 errors are
-// relative to the deviations from p, not to p.
+// Moments: every warp sums about its own mean, and the warps' sums are moved to
+// the token's mean (Chan's formula), so a mean much larger than the deviation
+// costs no accuracy and one exchange a token is enough. (The direct backward
+// sums about a pivot in each thread and adds in fp64.)
 //
 // hc_layernorm_kernel keeps a token's h in registers between the statistic and
 // the store, so H is read once. hc_layernorm_bwd_kernel parks h in shared
@@ -96,11 +95,25 @@ __global__ void __launch_bounds__(kFwdThreads)
 hc_layernorm_kernel(StepParams p, const float *beta) {
     constexpr int V = StorageTraits<S>::V, VP = V / 2;
     __shared__ float sa[kTB * N];
-    __shared__ double sums[2 * (kFwdThreads / 32) * 2];
+    // of alternate tokens: the warps' means, and their sums of squares and of h
+    // about them (the latter is what the mean's rounding left)
+    __shared__ float sums[2][3][32];
     __shared__ float swork[kFwdThreads / 32 * kGroupScratch];
     const int tid = threadIdx.x, NT = blockDim.x, nwarps = NT >> 5;
     const int lane = tid & 31, warp = tid >> 5;
     const int64_t d = p.d, nvec = d / V, G = gridDim.x;
+    auto warp_columns = [&](int w) {
+        int64_t n = 0;
+#pragma unroll
+        for (int u = 0; u < CPT; ++u) {
+            const int64_t left = d - ((int64_t)u * NT + w * 32) * V;
+            n += left < 0 ? 0 : left < 32 * V ? left : 32 * V;
+        }
+        return (float)n;
+    };
+    const float n_own = warp_columns(warp), inv_n = n_own > 0.0f ? 1.0f / n_own : 0.0f;
+    const float n_w = lane < nwarps ? warp_columns(lane) : 0.0f;  // lane w: warp w
+    const float inv_d = 1.0f / (float)d;
     int TB = nwarps * Group<N>::TPW;
     TB = TB < kTB ? TB : kTB;
     const S *H = static_cast<const S *>(p.H);
@@ -116,7 +129,7 @@ hc_layernorm_kernel(StepParams p, const float *beta) {
             const int64_t t = first + (int64_t)tt * G;
             if (t >= p.T) break;  // uniform over the CTA
             float2 h[CPT][VP];
-            Moments mo;
+            float wm = 0.0f;
 #pragma unroll
             for (int u = 0; u < CPT; ++u) {
                 const int64_t c = tid + (int64_t)u * NT;
@@ -133,19 +146,49 @@ hc_layernorm_kernel(StepParams p, const float *beta) {
 #pragma unroll
                         for (int e = 0; e < VP; ++e) h[u][e] = i == 0 ? fmul2_rn(ai, v[e]) : ffma2_rn(ai, v[e], h[u][e]);
                     }
-                    mo.add<VP>(h[u]);
+                    float2 z = h[u][0];
+#pragma unroll
+                    for (int e = 1; e < VP; ++e) z = fadd2_rn(z, h[u][e]);
+                    wm += z.x + z.y;
                 }
             }
-            double v[2] = {mo.sum(), mo.squares()};
-            cta_sums<2>(v, sums, parity, nwarps, lane, warp);
+            // the warp's mean, and h, its sum and squares about it
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) wm += __shfl_xor_sync(0xffffffffu, wm, o);
+            wm *= inv_n;
+            float2 q2 = make_float2(0.0f, 0.0f), l2 = q2;
+            const float2 nm = make_float2(-wm, -wm);
+#pragma unroll
+            for (int u = 0; u < CPT; ++u) {
+                if (tid + (int64_t)u * NT < nvec) {
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) {
+                        h[u][e] = fadd2_rn(h[u][e], nm);
+                        q2 = ffma2_rn(h[u][e], h[u][e], q2);
+                        l2 = fadd2_rn(l2, h[u][e]);
+                    }
+                }
+            }
+            const float v[2] = {q2.x + q2.y, l2.x + l2.y};
+            warp_sums_put<2>(v, lane, [&](int x, float sx) { sums[parity][1 + x][warp] = sx; });
+            if (lane == 0) sums[parity][0][warp] = wm;
+            __syncthreads();
+            // moved to the mean of all: lane w takes warp w's
+            const bool has = n_w > 0.0f;
+            const float m0 = sums[parity][0][0], dm = has ? sums[parity][0][lane] - m0 : 0.0f;
+            const float sl = has ? sums[parity][2][lane] : 0.0f, s2 = has ? sums[parity][1][lane] : 0.0f;
             parity ^= 1;
-            const double mu = v[0] / (double)d;
-            double var = v[1] / (double)d - mu * mu;
-            var = var < 0.0 ? 0.0 : var;  // rounding only (NaN stays)
-            const float rs = __double2float_rn(1.0 / sqrt(var + (double)p.eps)), muf = (float)mu;
-            // h - mu with mu's own rounding kept: two fp32 parts
-            const float mul = (float)(mu - (double)muf);
-            const float2 nm = make_float2(-muf, -muf), nl = make_float2(-mul, -mul), r2 = make_float2(rs, rs);
+            float mu = __fmaf_rn(n_w, dm, sl);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mu += __shfl_xor_sync(0xffffffffu, mu, o);
+            mu *= inv_d;  // the mean less m0
+            const float del = dm - mu;
+            float sq = __fmaf_rn(del, __fmaf_rn(n_w, del, 2.0f * sl), s2);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            const float rs = __frsqrt_rn(__fmaf_rn(sq < 0.0f ? 0.0f : sq, inv_d, p.eps));  // below 0: rounding only
+            const float own = (wm - m0) - mu;  // the warp's mean less the token's
+            const float2 nz = make_float2(own, own), r2 = make_float2(rs, rs);
 #pragma unroll
             for (int u = 0; u < CPT; ++u) {
                 const int64_t c = tid + (int64_t)u * NT;
@@ -155,7 +198,7 @@ hc_layernorm_kernel(StepParams p, const float *beta) {
                     if (beta) load_gain2<VP>(beta, c * V, bv);
 #pragma unroll
                     for (int e = 0; e < VP; ++e) {
-                        const float2 z = fmul2_rn(fadd2_rn(fadd2_rn(h[u][e], nm), nl), r2);
+                        const float2 z = fmul2_rn(fadd2_rn(h[u][e], nz), r2);
                         x[e] = beta ? ffma2_rn(z, gv[e], bv[e]) : fmul2_rn(z, gv[e]);
                     }
                     __stcs(reinterpret_cast<uint4 *>(X + t * d + c * V), ck_narrow(x));
