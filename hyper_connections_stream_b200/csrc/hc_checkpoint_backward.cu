@@ -49,45 +49,23 @@ template <int N> struct CkSums {
     static constexpr int B = N * N, U = B + N, H = U + N + 1, SS = H + N + 1, SG = SS + 1, COUNT = SG + 1;
 };
 
-// From the warps' partial sums (red [warps][COUNT]) to r and q in stat[0 .. 1];
-// called by one warp, which then writes the token's parameter gradients with
-// ck_write_params.
+// The token's parameter gradients from its sums (one warp).
 template <int N>
-__device__ __forceinline__ void ck_finish_sums(const float *red, int nwarps, double *fin, float *stat, int64_t d,
-                                               float eps, int lane) {
+__device__ __forceinline__ void ck_write_params(const float *fin, float r, float q, const float *At, const float *bt,
+                                                const float *at, float *gA, float *gb, float *ga, int64_t t,
+                                                int lane) {
     using Q = CkSums<N>;
-    for (int v = lane; v < Q::COUNT; v += 32) {
-        double s = 0.0;
-        for (int w = 0; w < nwarps; ++w) s += (double)red[w * Q::COUNT + v];
-        fin[v] = s;
-    }
-    __syncwarp();
-    if (lane == 0) {
-        const float r = __double2float_rn(1.0 / sqrt(fin[Q::SS] / (double)d + (double)eps));
-        const double rd = (double)r;
-        stat[0] = r;
-        stat[1] = (float)(rd * rd * rd * fin[Q::SG] / (double)d);
-    }
-    __syncwarp();
-}
-
-template <int N>
-__device__ __forceinline__ void ck_write_params(const double *fin, const float *stat, const float *At,
-                                                const float *bt, const float *at, float *gA, float *gb, float *ga,
-                                                int64_t t, int lane) {
-    using Q = CkSums<N>;
-    const double r = (double)stat[0], q = (double)stat[1];
     for (int e = lane; e < N * N; e += 32) {
         const int i = e / N, j = e - i * N;
-        gA[t * (N * N) + e] = (float)(fin[e] + (double)at[j] * (r * fin[Q::U + i] - q * fin[Q::H + i]));
+        gA[t * (N * N) + e] = fin[e] + at[j] * (r * fin[Q::U + i] - q * fin[Q::H + i]);
     }
     if (lane < N) {
-        const double py = r * fin[Q::U + N] - q * fin[Q::H + N];
-        gb[t * N + lane] = (float)(fin[Q::B + lane] + (double)at[lane] * py);
-        double s = (double)bt[lane] * py;
+        const float py = r * fin[Q::U + N] - q * fin[Q::H + N];
+        gb[t * N + lane] = fin[Q::B + lane] + at[lane] * py;
+        float s = bt[lane] * py;
 #pragma unroll
-        for (int i = 0; i < N; ++i) s += (double)At[i * N + lane] * (r * fin[Q::U + i] - q * fin[Q::H + i]);
-        ga[t * N + lane] = (float)s;
+        for (int i = 0; i < N; ++i) s += At[i * N + lane] * (r * fin[Q::U + i] - q * fin[Q::H + i]);
+        ga[t * N + lane] = s;
     }
     __syncwarp();
 }
@@ -105,9 +83,11 @@ hc_ck_bwd_kernel(CkBwParams bp) {
     using Q = CkSums<N>;
     constexpr int NV = Q::COUNT, NW = kThreads / 32;
     __shared__ float sA[kTB * NN], sb[kTB * N], sa[kTB * N], sc[kTB * (N + 1)];
-    __shared__ float red[NW * NV];
-    __shared__ double fin[NV];
-    __shared__ float stat[2];
+    // of alternate tokens: the warps' sums, and their two statistics side by side
+    __shared__ float red[2][NW * NV];
+    __shared__ __align__(16) float stat[2][2][8];
+    __shared__ float fin[NV];
+    static_assert(NW <= 8, "the statistics of eight warps");
     __shared__ float swork[NW * kGroupScratch];
     extern __shared__ __align__(16) float shp[];  // [d] parked h
 
@@ -128,6 +108,8 @@ hc_ck_bwd_kernel(CkBwParams bp) {
                 *reinterpret_cast<float4 *>(sdg + k + e) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
 
+    if (tid < 32) (&stat[0][0][0])[tid] = 0.0f;
+    int par = 0, turn = 0;
     for (int64_t m0 = 0;; m0 += TB) {
         const int64_t first = blockIdx.x + m0 * G;
         if (first >= p.T) break;
@@ -228,14 +210,23 @@ hc_ck_bwd_kernel(CkBwParams bp) {
                     }
                 }
             }
-            warp_sums_all<NV>(acc, red + warp * NV, lane);
+            warp_sums_all<NV>(acc, red[par] + warp * NV, lane);
+            __syncwarp();
+            if (lane < 2) stat[par][lane][warp] = red[par][warp * NV + Q::SS + lane];
             __syncthreads();
-            if (warp == 0) ck_finish_sums<N>(red, nwarps, fin, stat, d, p.eps, lane);
-            __syncthreads();
-            if (warp == 0) ck_write_params<N>(fin, stat, At, bt, at, bp.gA, bp.gb, bp.ga, t, lane);
+            float tot[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float4 f = *reinterpret_cast<const float4 *>(&stat[par][x][0]);
+                const float4 h4 = *reinterpret_cast<const float4 *>(&stat[par][x][4]);
+                tot[x] = ((f.x + h4.x) + (f.y + h4.y)) + ((f.z + h4.z) + (f.w + h4.w));
+            }
+            const float inv_d = 1.0f / (float)d;
+            const float r = __frsqrt_rn(__fmaf_rn(tot[0], inv_d, p.eps));
+            const float q = r * r * r * (tot[1] * inv_d);
 
             // ---- pass 2: the gradients of H and y ----
-            const float2 r2 = make_float2(stat[0], stat[0]), nq2 = make_float2(-stat[1], -stat[1]);
+            const float2 r2 = make_float2(r, r), nq2 = make_float2(-q, -q);
             for (int k = tid * V; k < d; k += NT * V) {
                 float2 dx[VP], gv[VP], h[VP], dh[VP];
                 ck_widen(__ldcs(reinterpret_cast<const uint4 *>(DXt + k)), dx);
@@ -287,6 +278,17 @@ hc_ck_bwd_kernel(CkBwParams bp) {
                     __stcs(reinterpret_cast<uint4 *>(DHt + (i * d + k)), ck_narrow(o[i]));
                 __stcs(reinterpret_cast<uint4 *>(DYt + k), ck_narrow(o[N]));
             }
+            if (warp == turn) {  // one warp a token, in turn, writes the parameter gradients
+                for (int v = lane; v < Q::SS; v += 32) {
+                    float a = 0.0f;
+                    for (int w = 0; w < nwarps; ++w) a += red[par][w * NV + v];
+                    fin[v] = a;
+                }
+                __syncwarp();
+                ck_write_params<N>(fin, r, q, At, bt, at, bp.gA, bp.gb, bp.ga, t, lane);
+            }
+            turn = turn + 1 == nwarps ? 0 : turn + 1;
+            par ^= 1;
         }
     }
 }
