@@ -16,10 +16,23 @@
 // after dh is known (H and y read and decoded twice, n^2 + n products each to
 // rebuild H') this leaves about half the arithmetic.
 //
-// hc_ck_bwd_kernel: a CTA takes a token at a time; threads own 16-byte column
-// slices. dH' and dx are read again from L2 in the second pass, h is parked in
-// shared memory (fp32; rebuilt from the checkpoint where a row does not fit).
-// The gain gradient accumulates in the CTA's workspace row.
+// hc_ck_bwd_kernel: a CTA takes a token at a time; threads own column slices of
+// 16 bytes of dH'. dH' and dx are read again from L2 in the second pass, h is
+// parked in shared memory (fp32; rebuilt from the checkpoint where a row does
+// not fit). The gain gradient accumulates in the CTA's workspace row. All sums
+// are fp32: a row whose squares overflow fp32 has no finite norm.
+//
+// Measured: T = 16384, n = 4, d = 7168, bf16 in 885 us with its parameter
+// kernels (51 % of the copy rate; 27 % fewer bytes but 10 % less time than the
+// bf16 backward), n = 8, T = 2048, d = 4096 in 184 us. It is held by latency: 14
+// warps of 128 registers on a multiprocessor, 39 % of the issue slots and of the
+// FMA pipes used, 99 instructions a column. What did not help at n = 4: whole
+// tokens or tiles of them through a bulk-copied ring (827 to 930 us: the
+// arithmetic took as long from shared memory, and the barriers came on top),
+// staging slices with cp.async (930 to 995), dH' and dx kept in shared memory
+// for the second pass (909), slices of half the width at 80 registers and three
+// CTAs (1054: half as many instructions again). The prefetch into L2 gains 16 %
+// at n = 8, where one CTA has a multiprocessor to itself.
 #include <atomic>
 
 #include "hc_checkpoint.cuh"

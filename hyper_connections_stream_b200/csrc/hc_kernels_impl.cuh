@@ -99,8 +99,10 @@ bool pipe_shape(const StepParams &p, int rows, PipeShape &sh, int &smem) {
                         ((int64_t)kPipeGroups * (sh.stage_bytes + 16));
     if (per_group < 2) return false;
     if (per_group > kMaxStages / kPipeGroups) per_group = kMaxStages / kPipeGroups;
-    const int64_t cap = KIND == KIND_WRITE ? HC_PIPE_SG_WRITE
-                        : KIND == KIND_FUSED || KIND == KIND_SAVE ? HC_PIPE_SG_FUSED
+    // (the saving step writes half as much again as it reads: the write kind's
+    // depth, 288 us against 292 at T = 8192, n = 4, d = 7168)
+    const int64_t cap = KIND == KIND_WRITE || KIND == KIND_SAVE ? HC_PIPE_SG_WRITE
+                        : KIND == KIND_FUSED ? HC_PIPE_SG_FUSED
                         : KIND == KIND_REDUCE ? HC_PIPE_SG_REDUCE : HC_PIPE_SG_READ;
     if (per_group > cap) per_group = cap;
     if (per_group < 1) per_group = 1;

@@ -352,8 +352,9 @@ HC_API hc_status hc_write_then_read_checkpoint(
  * Backward of hc_write_then_read from the checkpoint of its H and y: the
  * gradients of the step at the kept values, with H' not rounded to dt between
  * the write and the read (the kept values' own rounding is 2^-4, and the
- * gradients pass straight through every rounding). dt is the type of dHout,
- * dx, dH and dy. Arguments, outputs and the workspace rule (its size from
+ * gradients pass straight through every rounding). All sums in fp32 (squares
+ * of h that overflow it have no finite norm). dt is the type of dHout, dx, dH
+ * and dy. Arguments, outputs and the workspace rule (its size from
  * hc_write_then_read_backward_checkpoint_workspace_bytes) otherwise as
  * hc_write_then_read_backward. At n = 1 the norm cancels the read weight: its
  * gradient is rounding. T == 0 sets dg (if given) to zero and does nothing
@@ -374,8 +375,9 @@ HC_API size_t hc_write_then_read_backward_checkpoint_workspace_bytes(hc_dtype dt
  *   h = sum_i a_i H_i,  x = (h - mean(h)) / sqrt(mean((h - mean(h))^2) + eps) * g + beta
  *   beta: [d] fp32 or NULL for none, 16-byte aligned.
  *   a may be NULL when n == 1: weight 1, the plain layer norm of rows [T][d].
- * Other arguments as hc_read_rmsnorm. h in fp32, the moments in fp64 over
- * fp32 sums about a pivot, x rounded once.
+ * Other arguments as hc_read_rmsnorm. h and the moments in fp32 (sums about
+ * means, so a mean far from zero costs nothing; squares that overflow fp32,
+ * |h| above about 1e19, have no finite norm), x rounded once.
  */
 HC_API hc_status hc_read_layernorm(const void *H, void *x, hc_dtype dt, int64_t T, int n, int64_t d,
                                    hc_read_mode rm, const float *a, int64_t a_tok_stride, const float *g,
