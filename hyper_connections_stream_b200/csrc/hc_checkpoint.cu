@@ -5,7 +5,7 @@
 // Both are bound by memory: a value costs its own bytes and 1 + 1/32. Measured
 // for T = 16384, n = 4, d = 7168, bf16 (1.42 GB each way): packing 242 us, 92 %
 // of the copy rate by DRAM counters' bytes; unpacking, which writes twice what
-// it reads, 270 us alone, 72 % of the copy rate when it follows at once. Two or
+// it reads, 309 us under the profiler, 72 %, and about 270 us in the pair. Two or
 // eight chunks in flight a thread, plain instead of streaming stores, and eight
 // times the CTAs were 1 to 18 % slower. A warp
 // takes one 256-element chunk of a row at a time, 16 bytes of codes' worth a

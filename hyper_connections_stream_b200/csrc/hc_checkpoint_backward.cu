@@ -22,17 +22,16 @@
 // not fit). The gain gradient accumulates in the CTA's workspace row. All sums
 // are fp32: a row whose squares overflow fp32 has no finite norm.
 //
-// Measured: T = 16384, n = 4, d = 7168, bf16 in 885 us with its parameter
-// kernels (51 % of the copy rate; 27 % fewer bytes but 10 % less time than the
-// bf16 backward), n = 8, T = 2048, d = 4096 in 184 us. It is held by latency: 14
-// warps of 128 registers on a multiprocessor, 39 % of the issue slots and of the
-// FMA pipes used, 99 instructions a column. What did not help at n = 4: whole
-// tokens or tiles of them through a bulk-copied ring (827 to 930 us: the
-// arithmetic took as long from shared memory, and the barriers came on top),
-// staging slices with cp.async (930 to 995), dH' and dx kept in shared memory
-// for the second pass (909), slices of half the width at 80 registers and three
-// CTAs (1054: half as many instructions again). The prefetch into L2 gains 16 %
-// at n = 8, where one CTA has a multiprocessor to itself.
+// Measured: T = 16384, n = 4, d = 7168, bf16 in 894 us with its parameter
+// kernels (51 % of the copy rate), n = 8, T = 2048, d = 4096 in 179 us. It is
+// held by latency: 14 warps of 128 registers on a multiprocessor, 39 % of the
+// issue slots and of the FMA pipes used, 99 instructions a column. Whole tokens
+// through a bulk-copied ring are faster at that n = 4 case (733 us with ten
+// warps of 168 registers) and slower at d = 4096 and at n = 8. What did not help
+// there: staging slices with cp.async (930 to 995), dH' and dx kept in shared
+// memory for the second pass (909), slices of half the width at 80 registers and
+// three CTAs (1054: half as many instructions again). The prefetch into L2 gains
+// 16 % at n = 8, where one CTA has a multiprocessor to itself.
 #include <atomic>
 
 #include "hc_checkpoint.cuh"
