@@ -16,27 +16,27 @@
 // after dh is known (H and y read and decoded twice, n^2 + n products each to
 // rebuild H') this leaves about half the arithmetic.
 //
-// hc_ck_bwd_kernel: a CTA takes a token at a time; threads own column slices of
-// 16 bytes of dH'. dH' and dx are read again from L2 in the second pass, h is
-// parked in shared memory (fp32; rebuilt from the checkpoint where a row does
-// not fit). The gain gradient accumulates in the CTA's workspace row. All sums
-// are fp32: a row whose squares overflow fp32 has no finite norm.
+// hc_ck_bwd_ring_kernel (hc_checkpoint_ring.cuh) takes long rows of up to four
+// streams. hc_ck_bwd_kernel, here, takes the rest: a CTA takes a token at a
+// time; threads own column slices of 16 bytes of dH'. dH' and dx are read again
+// from L2 in the second pass, h is parked in shared memory (fp32; rebuilt from
+// the checkpoint where a row does not fit). The gain gradient accumulates in the
+// CTA's workspace row. All sums are fp32: a row whose squares overflow fp32 has
+// no finite norm.
 //
-// Measured: T = 16384, n = 4, d = 7168, bf16 in 894 us with its parameter
-// kernels (51 % of the copy rate), n = 8, T = 2048, d = 4096 in 179 us. It is
-// held by latency: 14 warps of 128 registers on a multiprocessor, 39 % of the
-// issue slots and of the FMA pipes used, 99 instructions a column. Whole tokens
-// through a bulk-copied ring are faster at that n = 4 case (733 us with ten
-// warps of 168 registers) and slower at d = 4096 and at n = 8. What did not help
-// there: staging slices with cp.async (930 to 995), dH' and dx kept in shared
-// memory for the second pass (909), slices of half the width at 80 registers and
-// three CTAs (1054: half as many instructions again). The prefetch into L2 gains
-// 16 % at n = 8, where one CTA has a multiprocessor to itself.
+// Measured: n = 8, T = 2048, d = 4096, bf16 in 179 us with the parameter kernels;
+// n = 4, T = 16384, d = 7168 in 894 us, which the ring does in 708 (64 % of the
+// copy rate). The direct kernel is
+// held by latency: 14 warps of 128 registers on a multiprocessor at n = 4, 39 %
+// of the issue slots and of the FMA pipes used, 99 instructions a column. What
+// did not help there: staging slices with cp.async (930 to 995), dH' and dx kept
+// in shared memory for the second pass (909), slices of half the width at 80
+// registers and three CTAs (1054: half as many instructions again). The prefetch
+// into L2 gains 16 % at n = 8, where one CTA has a multiprocessor to itself.
 #include <atomic>
 
-#include "hc_checkpoint.cuh"
+#include "hc_checkpoint_ring.cuh"
 #include "hc_launch.h"
-#include "hc_token_sums.cuh"
 
 namespace hc {
 
@@ -44,43 +44,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTB = 32;  // parameter slots per batch
-
-struct CkBwParams {
-    StepParams f;          // H and y hold the codes
-    const uint8_t *sH, *sy;
-    int64_t ns;            // exponent bytes per row
-    const void *dHout, *dx;
-    void *dH, *dy;
-    float *gA, *gb, *ga;   // per-token sums (w.r.t. the matrix and the weights)
-    float *dg_part;        // [gridDim.x][d] or null
-};
-
-// Sums of a token, in this order: dA [n][n], db [n], <u, H_i> and <u, y>
-// [n + 1], <h, H_i> and <h, y> [n + 1], sum h^2, sum u h.
-template <int N> struct CkSums {
-    static constexpr int B = N * N, U = B + N, H = U + N + 1, SS = H + N + 1, SG = SS + 1, COUNT = SG + 1;
-};
-
-// The token's parameter gradients from its sums (one warp).
-template <int N>
-__device__ __forceinline__ void ck_write_params(const float *fin, float r, float q, const float *At, const float *bt,
-                                                const float *at, float *gA, float *gb, float *ga, int64_t t,
-                                                int lane) {
-    using Q = CkSums<N>;
-    for (int e = lane; e < N * N; e += 32) {
-        const int i = e / N, j = e - i * N;
-        gA[t * (N * N) + e] = fin[e] + at[j] * (r * fin[Q::U + i] - q * fin[Q::H + i]);
-    }
-    if (lane < N) {
-        const float py = r * fin[Q::U + N] - q * fin[Q::H + N];
-        gb[t * N + lane] = fin[Q::B + lane] + at[lane] * py;
-        float s = bt[lane] * py;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s += At[i * N + lane] * (r * fin[Q::U + i] - q * fin[Q::H + i]);
-        ga[t * N + lane] = s;
-    }
-    __syncwarp();
-}
 
 // Ask for `bytes` at p to be brought into L2 (both multiples of 16).
 __device__ __forceinline__ void prefetch_l2(const void *p, int64_t bytes) {
@@ -297,7 +260,7 @@ hc_ck_bwd_kernel(CkBwParams bp) {
                     fin[v] = a;
                 }
                 __syncwarp();
-                ck_write_params<N>(fin, r, q, At, bt, at, bp.gA, bp.gb, bp.ga, t, lane);
+                ck_write_params<N, false>(fin, r, q, At, bt, at, bp.gA, bp.gb, bp.ga, t, lane);
             }
             turn = turn + 1 == nwarps ? 0 : turn + 1;
             par ^= 1;
@@ -308,6 +271,46 @@ hc_ck_bwd_kernel(CkBwParams bp) {
 template <int N, typename S>
 struct CkBw {
     static constexpr int V = StorageTraits<S>::V;
+    // The ring takes rows from 640 slices up, where ten warps have two full
+    // slices a thread. Direct -> ring, 268 MB of values a call, n = 4: bf16 d =
+    // 2048 251 -> 287, 4096 228 -> 235, 5120 252 -> 216, 7168 261 -> 199 us; fp32
+    // d = 2048 162 -> 174, 2560 203 -> 156, 3840 224 -> 140 us; n = 2 and 3 alike.
+    // With one fp32 stream a row is too little for one CTA a multiprocessor
+    // (82 -> 95 us at 2560, 86 -> 88 at 3200). Beyond n = 4 a thread's sums
+    // alone fill the registers.
+    static constexpr int64_t kRingFrom = 640 * V;
+    static constexpr bool RINGS = N <= 4 && !(N == 1 && V == 4);
+    // The ring's geometry for rows of d; no stages where the direct kernel takes them.
+    static CkRingShape ring(int64_t d, int64_t &smem) {
+        CkRingShape sh{};
+        if (!RINGS || d % 16 != 0 || d < kRingFrom) return sh;
+        const int64_t nvec = d / V;
+        const int64_t slices = (nvec + 32 * kCkWarps - 1) / (32 * kCkWarps);
+        if (slices > kCkSlices) return sh;
+        sh.gw = (int)((nvec + 32 * slices - 1) / (32 * slices));
+        sh.stage_bytes = (N + 1) * (d * (int64_t)sizeof(S) + d + ck_scale_stride(d));
+        int64_t nst = (kSmemLimitLogits - ck_ring_fixed_bytes<N>(0)) / (sh.stage_bytes + 16);
+        if (nst < 2) return sh;
+        if (nst > 4) nst = 4;
+        sh.nst = (int)nst;
+        smem = nst * sh.stage_bytes + ck_ring_fixed_bytes<N>((int)nst);
+        return sh;
+    }
+    // Dynamic shared memory opted in once per device, at its most.
+    static hc_status configure_ring(const LaunchCtx &ctx) {
+        if constexpr (RINGS) {
+            static std::atomic<bool> done[64];
+            if (ctx.device < 0 || ctx.device >= 64)
+                return set_error(HC_ERR_UNSUPPORTED, "device ordinal %d >= 64", ctx.device);
+            if (done[ctx.device].load()) return HC_OK;
+            const cudaError_t e = cudaFuncSetAttribute(
+                hc_ck_bwd_ring_kernel<N, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimitLogits);
+            if (e != cudaSuccess)
+                return set_error(HC_ERR_CUDA, "checkpoint backward smem attribute: %s", cudaGetErrorString(e));
+            done[ctx.device].store(true);
+        }
+        return HC_OK;
+    }
     // h parked up to 96 KB of d: two CTAs a multiprocessor at n <= 4
     static bool parked(int64_t d) { return d * 4 <= 96 * 1024; }
     static int threads(int64_t d) {
@@ -333,6 +336,11 @@ struct CkBw {
         return HC_OK;
     }
     static hc_status grid(int64_t T, int64_t d, const LaunchCtx &ctx, int64_t &grid) {
+        int64_t smem = 0;
+        if (ring(d, smem).nst) {
+            grid = ctx.sms < T ? ctx.sms : T;
+            return configure_ring(ctx);
+        }
         const bool park = parked(d);
         const hc_status s = park ? configure<true>(ctx) : configure<false>(ctx);
         if (s != HC_OK) return s;
@@ -350,7 +358,7 @@ struct CkBw {
         return HC_OK;
     }
     static hc_status launch(const BackwardArgs &a, const uint8_t *sH, const uint8_t *sy, int64_t g,
-                            cudaStream_t st) {
+                            const LaunchCtx &ctx, cudaStream_t st) {
         CkBwParams bp{};
         bp.f = a.f;
         bp.sH = sH;
@@ -364,6 +372,17 @@ struct CkBw {
         bp.gb = a.db;
         bp.ga = a.da;
         bp.dg_part = a.dg ? static_cast<float *>(a.workspace) : nullptr;
+        if constexpr (RINGS) {
+            int64_t smem = 0;
+            const CkRingShape sh = ring(a.f.d, smem);
+            if (sh.nst) {
+                hc_ck_bwd_ring_kernel<N, S><<<(unsigned)g, 32 * (2 + kCkWarps), (size_t)smem, st>>>(bp, sh, ctx.fault);
+                const cudaError_t e = cudaGetLastError();
+                if (e != cudaSuccess)
+                    return set_error(HC_ERR_CUDA, "hc_ck_bwd_ring_kernel launch: %s", cudaGetErrorString(e));
+                return HC_OK;
+            }
+        }
         const int NT = threads(a.f.d);
         if (parked(a.f.d)) hc_ck_bwd_kernel<N, S, true><<<(unsigned)g, NT, (size_t)a.f.d * 4, st>>>(bp);
         else hc_ck_bwd_kernel<N, S, false><<<(unsigned)g, NT, 0, st>>>(bp);
@@ -378,9 +397,10 @@ hc_status grid_n(hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx, int64_
     return dt == HC_BF16 ? CkBw<N, __nv_bfloat16>::grid(T, d, ctx, g) : CkBw<N, float>::grid(T, d, ctx, g);
 }
 template <int N>
-hc_status launch_n(const BackwardArgs &a, const uint8_t *sH, const uint8_t *sy, int64_t g, cudaStream_t st) {
-    return a.dt == HC_BF16 ? CkBw<N, __nv_bfloat16>::launch(a, sH, sy, g, st)
-                           : CkBw<N, float>::launch(a, sH, sy, g, st);
+hc_status launch_n(const BackwardArgs &a, const uint8_t *sH, const uint8_t *sy, int64_t g,
+                   const LaunchCtx &ctx, cudaStream_t st) {
+    return a.dt == HC_BF16 ? CkBw<N, __nv_bfloat16>::launch(a, sH, sy, g, ctx, st)
+                           : CkBw<N, float>::launch(a, sH, sy, g, ctx, st);
 }
 
 hc_status grid_of(int n, hc_dtype dt, int64_t T, int64_t d, const LaunchCtx &ctx, int64_t &g) {
@@ -418,14 +438,14 @@ hc_status launch_checkpoint_backward(const BackwardArgs &a, const uint8_t *sH, c
     if (a.dg && a.workspace_bytes < need)
         return set_error(HC_ERR_INVALID_ARG, "workspace of %zu bytes < %zu needed for dg", a.workspace_bytes, need);
     switch (a.n) {
-        case 1: s = launch_n<1>(a, sH, sy, g, st); break;
-        case 2: s = launch_n<2>(a, sH, sy, g, st); break;
-        case 3: s = launch_n<3>(a, sH, sy, g, st); break;
-        case 4: s = launch_n<4>(a, sH, sy, g, st); break;
-        case 5: s = launch_n<5>(a, sH, sy, g, st); break;
-        case 6: s = launch_n<6>(a, sH, sy, g, st); break;
-        case 7: s = launch_n<7>(a, sH, sy, g, st); break;
-        default: s = launch_n<8>(a, sH, sy, g, st); break;
+        case 1: s = launch_n<1>(a, sH, sy, g, ctx, st); break;
+        case 2: s = launch_n<2>(a, sH, sy, g, ctx, st); break;
+        case 3: s = launch_n<3>(a, sH, sy, g, ctx, st); break;
+        case 4: s = launch_n<4>(a, sH, sy, g, ctx, st); break;
+        case 5: s = launch_n<5>(a, sH, sy, g, ctx, st); break;
+        case 6: s = launch_n<6>(a, sH, sy, g, ctx, st); break;
+        case 7: s = launch_n<7>(a, sH, sy, g, ctx, st); break;
+        default: s = launch_n<8>(a, sH, sy, g, ctx, st); break;
     }
     if (s != HC_OK) return s;
     return launch_backward_tail(a, g, ctx, st);

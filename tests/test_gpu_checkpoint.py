@@ -277,6 +277,61 @@ def test_backward_without_dHout_or_gain(hc, n, d, dt):
     _check_backward(hc, got, *case, sums=False)
 
 
+# rows that are copied whole into shared memory: one to three slices a thread,
+# two to four stages, rows at both ends of that range, fewer tokens than CTAs,
+# several a CTA, and more than the parameter slots hold
+@pytest.mark.parametrize("T,n,d,dt,mix,read,shared", [
+    (1, 4, 7168, "bf16", True, True, False),
+    (450, 4, 7168, "bf16", True, True, False),
+    (149, 4, 5136, "bf16", False, True, True),
+    (300, 3, 7664, "bf16", True, False, False),
+    (300, 2, 7680, "bf16", True, True, False),
+    (150, 1, 5136, "bf16", False, False, False),
+    (300, 4, 2576, "f32", True, True, False),
+    (150, 3, 3840, "f32", True, True, True),
+    (2600, 3, 2592, "f32", False, True, False),
+    (400, 2, 2592, "f32", True, False, False),
+])
+def test_backward_of_rows_in_shared_memory(hc, T, n, d, dt, mix, read, shared):
+    case = _backward_case(hc, T, n, d, dt, mix, read, shared, seed=700 + T + n)
+    got = hc.write_then_read_backward_checkpoint(*case[:8], **case[8])
+    again = hc.write_then_read_backward_checkpoint(*case[:8], **case[8])
+    for k in got:
+        assert torch.equal(got[k], again[k]), k
+    _check_backward(hc, got, *case)
+    assert hc.device_fault() == 0
+
+
+@pytest.mark.parametrize("n,d,dt", [(4, 5648, "bf16"), (2, 7168, "bf16"), (3, 2992, "f32")])
+def test_backward_of_rows_in_shared_memory_without_dHout_or_gain(hc, n, d, dt):
+    case = _backward_case(hc, 200, n, d, dt, True, True, False, 800, with_dHout=False, K=3)
+    _check_backward(hc, hc.write_then_read_backward_checkpoint(*case[:8], **case[8]), *case)
+    case = _backward_case(hc, 200, n, d, dt, False, True, False, 810, gain=False)
+    _check_backward(hc, hc.write_then_read_backward_checkpoint(*case[:8], **case[8]), *case)
+
+
+def test_backward_of_rows_in_shared_memory_on_streams_and_in_a_graph(hc):
+    case = _backward_case(hc, 320, 4, 7168, "bf16", True, True, False, 820)
+    other = _backward_case(hc, 310, 3, 5648, "bf16", False, True, False, 830)
+    want = [hc.write_then_read_backward_checkpoint(*c[:8], **c[8]) for c in (case, other)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for c, s in zip((case, other), streams):
+        with torch.cuda.stream(s):
+            got.append(hc.write_then_read_backward_checkpoint(*c[:8], **c[8]))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = hc.write_then_read_backward_checkpoint(*case[:8], **case[8])
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for k in want[0]:
+        assert torch.equal(got[0][k], want[0][k]) and torch.equal(got[1][k], want[1][k]), k
+        assert torch.equal(out[k], want[0][k]), k
+
+
 def test_backward_against_differences(hc):
     """Central differences of the fp64 step at the kept values, along random
     directions of every input (h^2 / 6 times the third derivative is below
