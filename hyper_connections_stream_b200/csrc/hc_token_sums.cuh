@@ -1,6 +1,6 @@
-// hc_token_sums.cuh -- sums of many per-thread values over a CTA: warp trees
-// in fp32, then the warps in order in fp64. The order is fixed by the launch
-// shape, so results are reproducible.
+// hc_token_sums.cuh -- sums of many per-thread values over a warp, as trees in
+// fp32; the kernels add the warps' sums in a fixed order. The order follows from
+// the launch shape, so results are reproducible.
 #pragma once
 
 #include "hc_backward_common.cuh"
