@@ -6,10 +6,10 @@
 // rounded. With H' linear in H and y so is h, and everything that multiplies
 // them can be summed before the token's statistic is known:
 //   h    = sum_i c_i H_i + c_y y,      c_i = sum_j A_ij a_j, c_y = sum_j a_j b_j
-//   u    = g dx,   dh = r u - q h,     q = (r^3 / d) sum u h
-//   P_i  = <dh, H_i> = r <u, H_i> - q <h, H_i>,   P_y likewise with y
+//   u    = g dx,   dh = r u - k z,     z = r h,  k = r mean(u z)
+//   P_i  = <dh, H_i> = r <u, H_i> - k (r <h, H_i>),   P_y likewise with y
 //   dA_ij = <H_i, dH'_j> + a_j P_i     db_j = <y, dH'_j> + a_j P_y
-//   da_j  = sum_i A_ij P_i + b_j P_y   dg = sum_t dx h r
+//   da_j  = sum_i A_ij P_i + b_j P_y   dg = sum_t dx z
 //   dH_i = sum_j A_ij dH'_j + c_i dh   dy = sum_j b_j dH'_j + c_y dh
 // So the first pass over a token takes n^2 + 3n + 4 sums and the checkpoint is
 // read there only; the second needs dH', dx and h. Against taking the sums
@@ -21,8 +21,8 @@
 // time; threads own column slices of 16 bytes of dH'. dH' and dx are read again
 // from L2 in the second pass, h is parked in shared memory (fp32; rebuilt from
 // the checkpoint where a row does not fit). The gain gradient accumulates in the
-// CTA's workspace row. All sums are fp32: a row whose squares overflow fp32 has
-// no finite norm.
+// CTA's workspace row. All sums are fp32: a row whose squares overflow it has no
+// norm, and NaN gradients (hc_checkpoint_ring.cuh).
 //
 // Measured: n = 8, T = 2048, d = 4096, bf16 in 179 us with the parameter kernels;
 // n = 4, T = 16384, d = 7168 in 894 us, which the ring does in 708 (64 % of the
@@ -72,6 +72,7 @@ hc_ck_bwd_kernel(CkBwParams bp) {
     const int d = (int)p.d, ns = (int)bp.ns;  // columns and a token's rows fit 32 bits
     int TB = nwarps * Group<N>::TPW;
     TB = TB < kTB ? TB : kTB;
+    const float inv_d = 1.0f / (float)d;
     const uint8_t *QH = static_cast<const uint8_t *>(p.H), *QY = static_cast<const uint8_t *>(p.y);
     const S *DX = static_cast<const S *>(bp.dx), *DHO = static_cast<const S *>(bp.dHout);
     S *DH = static_cast<S *>(bp.dH), *DY = static_cast<S *>(bp.dy);
@@ -185,6 +186,7 @@ hc_ck_bwd_kernel(CkBwParams bp) {
                     }
                 }
             }
+            ck_means<N>(acc, inv_d);
             warp_sums_all<NV>(acc, red[par] + warp * NV, lane);
             __syncwarp();
             if (lane < 2) stat[par][lane][warp] = red[par][warp * NV + Q::SS + lane];
@@ -196,12 +198,10 @@ hc_ck_bwd_kernel(CkBwParams bp) {
                 const float4 h4 = *reinterpret_cast<const float4 *>(&stat[par][x][4]);
                 tot[x] = ((f.x + h4.x) + (f.y + h4.y)) + ((f.z + h4.z) + (f.w + h4.w));
             }
-            const float inv_d = 1.0f / (float)d;
-            const float r = __frsqrt_rn(__fmaf_rn(tot[0], inv_d, p.eps));
-            const float q = r * r * r * (tot[1] * inv_d);
+            const CkStat sv = ck_stat(tot[0], tot[1], p.eps);
 
             // ---- pass 2: the gradients of H and y ----
-            const float2 r2 = make_float2(r, r), nq2 = make_float2(-q, -q);
+            const float2 r2 = make_float2(sv.r, sv.r), nk2 = make_float2(-sv.k, -sv.k);
             for (int k = tid * V; k < d; k += NT * V) {
                 float2 dx[VP], gv[VP], h[VP], dh[VP];
                 ck_widen(__ldcs(reinterpret_cast<const uint4 *>(DXt + k)), dx);
@@ -219,14 +219,17 @@ hc_ck_bwd_kernel(CkBwParams bp) {
                     mix_h(hv, h);
                 }
 #pragma unroll
-                for (int e = 0; e < VP; ++e) dh[e] = ffma2_rn(nq2, h[e], fmul2_rn(r2, fmul2_rn(dx[e], gv[e])));
+                for (int e = 0; e < VP; ++e) {
+                    h[e] = fmul2_rn(r2, h[e]);  // z
+                    dh[e] = ffma2_rn(nk2, h[e], fmul2_rn(r2, fmul2_rn(dx[e], gv[e])));
+                }
                 if (sdg) {
 #pragma unroll
                     for (int e = 0; e < VP; e += 2) {
                         float4 *pd = reinterpret_cast<float4 *>(sdg + k + 2 * e);
                         const float4 f = *pd;
-                        const float2 s0 = ffma2_rn(fmul2_rn(dx[e], h[e]), r2, make_float2(f.x, f.y));
-                        const float2 s1 = ffma2_rn(fmul2_rn(dx[e + 1], h[e + 1]), r2, make_float2(f.z, f.w));
+                        const float2 s0 = ffma2_rn(dx[e], h[e], make_float2(f.x, f.y));
+                        const float2 s1 = ffma2_rn(dx[e + 1], h[e + 1], make_float2(f.z, f.w));
                         *pd = make_float4(s0.x, s0.y, s1.x, s1.y);
                     }
                 }
@@ -260,7 +263,7 @@ hc_ck_bwd_kernel(CkBwParams bp) {
                     fin[v] = a;
                 }
                 __syncwarp();
-                ck_write_params<N, false>(fin, r, q, At, bt, at, bp.gA, bp.gb, bp.ga, t, lane);
+                ck_write_params<N, false>(fin, sv, (float)d, At, bt, at, bp.gA, bp.gb, bp.ga, t, lane);
             }
             turn = turn + 1 == nwarps ? 0 : turn + 1;
             par ^= 1;

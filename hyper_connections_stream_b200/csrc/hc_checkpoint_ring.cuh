@@ -41,28 +41,50 @@ struct CkBwParams {
 };
 
 // Sums of a token, in this order: dA [n][n], db [n], <u, H_i> and <u, y>
-// [n + 1], <h, H_i> and <h, y> [n + 1], sum h^2, sum u h.
+// [n + 1], <h, H_i> and <h, y> [n + 1], sum h^2, sum u h. The products with h
+// leave a thread divided by d: a mean fits fp32 wherever a thread's own columns
+// do (|h| to 1e18), the sum over a row would not.
 template <int N> struct CkSums {
     static constexpr int B = N * N, U = B + N, H = U + N + 1, SS = H + N + 1, SG = SS + 1, COUNT = SG + 1;
 };
 
+template <int N>
+__device__ __forceinline__ void ck_means(float (&acc)[CkSums<N>::COUNT], float inv_d) {
+#pragma unroll
+    for (int x = CkSums<N>::H; x < CkSums<N>::COUNT; ++x) acc[x] *= inv_d;
+}
+
+// A token's two statistics from mean h^2 and mean(u h): r = (mean h^2 +
+// eps)^(-1/2) and k = r mean(u z) with z = r h, so that dh = r u - k z. z and u z
+// are of ordinary size however far h is from 1; r^3, which dh = r u - (r^3
+// mean(u h)) h would take, leaves fp32's range below |h| = 1e-13 and above 1e12.
+struct CkStat {
+    float r, k;
+};
+__device__ __forceinline__ CkStat ck_stat(float mean_hh, float mean_uh, float eps) {
+    const float r = inv_norm(mean_hh, eps);
+    return {r, r * (r * mean_uh)};
+}
+
 // The token's parameter gradients from its sums (one warp). TR: At holds A
 // transposed.
 template <int N, bool TR>
-__device__ __forceinline__ void ck_write_params(const float *fin, float r, float q, const float *At, const float *bt,
-                                                const float *at, float *gA, float *gb, float *ga, int64_t t,
-                                                int lane) {
+__device__ __forceinline__ void ck_write_params(const float *fin, CkStat st, float d, const float *At,
+                                                const float *bt, const float *at, float *gA, float *gb, float *ga,
+                                                int64_t t, int lane) {
     using Q = CkSums<N>;
+    // <dh, row x>
+    auto along = [&](int x) { return st.r * fin[Q::U + x] - st.k * (st.r * fin[Q::H + x] * d); };
     for (int e = lane; e < N * N; e += 32) {
         const int i = e / N, j = e - i * N;
-        gA[t * (N * N) + e] = fin[e] + at[j] * (r * fin[Q::U + i] - q * fin[Q::H + i]);
+        gA[t * (N * N) + e] = fin[e] + at[j] * along(i);
     }
     if (lane < N) {
-        const float py = r * fin[Q::U + N] - q * fin[Q::H + N];
+        const float py = along(N);
         gb[t * N + lane] = fin[Q::B + lane] + at[lane] * py;
         float s = bt[lane] * py;
 #pragma unroll
-        for (int i = 0; i < N; ++i) s += At[TR ? lane * N + i : i * N + lane] * (r * fin[Q::U + i] - q * fin[Q::H + i]);
+        for (int i = 0; i < N; ++i) s += At[TR ? lane * N + i : i * N + lane] * along(i);
         ga[t * N + lane] = s;
     }
     __syncwarp();
@@ -194,6 +216,7 @@ hc_ck_bwd_ring_kernel(CkBwParams bp, CkRingShape sh, int *fault) {
     const int oq = (int)o_qh, os = (int)o_sh, odx = (int)o_dx;
     const int k0 = threadIdx.x * V, kstep = GW * 32 * V;  // first column, columns between a thread's slices
     S *DH = static_cast<S *>(bp.dH), *DY = static_cast<S *>(bp.dy);
+    const float inv_d = 1.0f / (float)d;
     float2 dga[CPT][VP];
 #pragma unroll
     for (int u = 0; u < CPT; ++u)
@@ -294,6 +317,7 @@ hc_ck_bwd_ring_kernel(CkBwParams bp, CkRingShape sh, int *fault) {
         // h lies where the producer's next copy lands: order the proxies (here,
         // where no stores to global memory are outstanding)
         if constexpr (IN_CODES) fence_proxy_async_smem();
+        ck_means<N>(acc, inv_d);
         // the two statistics first: the others' exchange overlaps the wait for them
         float *stat = stat_all + par * 2 * kCkStat;
         {
@@ -326,12 +350,10 @@ hc_ck_bwd_ring_kernel(CkBwParams bp, CkRingShape sh, int *fault) {
         float tot[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) tot[x] = sum16(stat + x * kCkStat);
-        const float inv_d = 1.0f / (float)d;
-        const float r = __frsqrt_rn(__fmaf_rn(tot[0], inv_d, p.eps));
-        const float q = r * r * r * (tot[1] * inv_d);
+        const CkStat sv = ck_stat(tot[0], tot[1], p.eps);
 
         // ---- pass 2: the gradients of H and y ----
-        const float2 r2 = make_float2(r, r), nq2 = make_float2(-q, -q);
+        const float2 r2 = make_float2(sv.r, sv.r), nk2 = make_float2(-sv.k, -sv.k);
         S *DHt = DH + t * N * d, *DYt = DY + t * d;
 #pragma unroll
         for (int u = 0; u < CPT; ++u) {
@@ -355,9 +377,9 @@ hc_ck_bwd_ring_kernel(CkBwParams bp, CkRingShape sh, int *fault) {
                 }
 #pragma unroll
                 for (int e = 0; e < VP; ++e) {
-                    const float2 rx = fmul2_rn(r2, dx[e]);
-                    dga[u][e] = ffma2_rn(rx, h[e], dga[u][e]);
-                    dh[e] = ffma2_rn(nq2, h[e], fmul2_rn(rx, gv[e]));
+                    const float2 z = fmul2_rn(r2, h[e]);
+                    dga[u][e] = ffma2_rn(dx[e], z, dga[u][e]);
+                    dh[e] = ffma2_rn(nk2, z, fmul2_rn(r2, fmul2_rn(dx[e], gv[e])));
                 }
                 if (u + 1 < CPT) fetch_gain(u + 1);
                 float2 o[N + 1][VP];
@@ -399,7 +421,7 @@ hc_ck_bwd_ring_kernel(CkBwParams bp, CkRingShape sh, int *fault) {
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(sumfree);
-            ck_write_params<N, true>(fin, r, q, P, bt, at, bp.gA, bp.gb, bp.ga, t, lane);
+            ck_write_params<N, true>(fin, sv, (float)d, P, bt, at, bp.gA, bp.gb, bp.ga, t, lane);
         }
         if (lane == 0) mbar_arrive(&pempty[ps]);
         turn = turn + 1 == GW ? 0 : turn + 1;

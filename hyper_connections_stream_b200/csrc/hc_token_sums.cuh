@@ -47,6 +47,13 @@ __device__ __forceinline__ void warp_sums_put(const float (&v)[M], int lane, Put
     if (lane % span == 0 && idx < M) put(idx, s);
 }
 
+// (m + eps)^(-1/2) of a mean square m; NaN where m is not finite (a row that
+// holds an infinity, or whose squares overflow, has no norm: its inverse is not
+// to pass for 0).
+__device__ __forceinline__ float inv_norm(float m, float eps) {
+    return m < INFINITY ? __frsqrt_rn(m + eps) : m - m;
+}
+
 // Sum of 16 floats in shared memory (16-byte aligned).
 __device__ __forceinline__ float sum16(const float *p) {
     const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);

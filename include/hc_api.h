@@ -352,8 +352,10 @@ HC_API hc_status hc_write_then_read_checkpoint(
  * Backward of hc_write_then_read from the checkpoint of its H and y: the
  * gradients of the step at the kept values, with H' not rounded to dt between
  * the write and the read (the kept values' own rounding is 2^-4, and the
- * gradients pass straight through every rounding). All sums in fp32 (squares
- * of h that overflow it have no finite norm). dt is the type of dHout, dx, dH
+ * gradients pass straight through every rounding). All sums in fp32: a row
+ * with |h| beyond about 1e18, whose squares overflow it, has NaN gradients, and
+ * with eps = 0 a row below about 1e-17 loses accuracy as its squares
+ * underflow. dt is the type of dHout, dx, dH
  * and dy. Arguments, outputs and the workspace rule (its size from
  * hc_write_then_read_backward_checkpoint_workspace_bytes) otherwise as
  * hc_write_then_read_backward. At n = 1 the norm cancels the read weight: its
