@@ -605,11 +605,11 @@ struct StepBw {
         return HC_OK;
     }
     template <int MD>
-    static hc_status occupancy(int NT, size_t dyn, int &per_sm) {
+    static hc_status occupancy(int NT, size_t dyn, const LaunchCtx &ctx, int &per_sm) {
         auto kern = kernel<MD>();
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn);
-        if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "backward smem attribute: %s", cudaGetErrorString(e));
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, NT, dyn);
+        static std::atomic<bool> done[64];
+        HC_BW_TRY(opt_in_smem(reinterpret_cast<const void *>(kern), (int)kDynBudget, done, ctx));
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, NT, dyn);
         if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "occupancy query: %s", cudaGetErrorString(e));
         return HC_OK;
     }
@@ -649,25 +649,26 @@ struct StepBw {
             return set_error(HC_ERR_UNSUPPORTED, "d = %lld too large for the backward", (long long)d);
         int per_sm = 0;
         const int md = mode(d, NT);
-        HC_BW_TRY(md == 2 ? occupancy<2>(NT, dyn, per_sm)
-                          : md == 1 ? occupancy<1>(NT, dyn, per_sm) : occupancy<0>(NT, dyn, per_sm));
+        HC_BW_TRY(md == 2 ? occupancy<2>(NT, dyn, ctx, per_sm)
+                          : md == 1 ? occupancy<1>(NT, dyn, ctx, per_sm) : occupancy<0>(NT, dyn, ctx, per_sm));
         if (per_sm < 1) per_sm = 1;
         grid = (int64_t)ctx.sms * per_sm;
         if (grid > T) grid = T;
         if (grid < 1) grid = 1;
         return HC_OK;
     }
+    static constexpr size_t kHistMost = (size_t)kSmemLimitLogits - 4096;
     // Threads and shared memory of the parameter backward: the Sinkhorn
     // backward's iterates must fit (checked before any launch).
     static hc_status param_shape(const BackwardArgs &a, size_t &hist, int &pthreads) {
         pthreads = 128;
         const int Kh = a.f.mix_logits ? a.f.K : 0;
         hist = (size_t)(2 * Kh + 1) * pthreads * Group<N>::EPL * 4;
-        if (hist > (size_t)kSmemLimitLogits - 4096) {
+        if (hist > kHistMost) {
             pthreads = 32;
             hist = (size_t)(2 * Kh + 1) * pthreads * Group<N>::EPL * 4;
         }
-        if (hist > (size_t)kSmemLimitLogits - 4096)
+        if (hist > kHistMost)
             return set_error(HC_ERR_UNSUPPORTED, "K = %d too large for the Sinkhorn backward", a.f.K);
         return HC_OK;
     }
@@ -694,16 +695,8 @@ struct StepBw {
                 if (!a.dHout) ps.gstages = 0;
                 const int64_t smem = bwp_smem_bytes<N>(ps.ntile, ps.gstages, want_dg);
                 auto kern = hc_bwd_pipe_kernel<N>;
-                static std::atomic<int> configured[64];  // largest opt-in so far, per device
-                if (ctx.device < 0 || ctx.device >= 64)
-                    return set_error(HC_ERR_UNSUPPORTED, "device ordinal %d >= 64", ctx.device);
-                if (smem > configured[ctx.device].load()) {
-                    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                         (int)smem);
-                    if (e != cudaSuccess)
-                        return set_error(HC_ERR_CUDA, "backward smem attribute: %s", cudaGetErrorString(e));
-                    configured[ctx.device].store((int)smem);
-                }
+                static std::atomic<bool> done[64];
+                HC_BW_TRY(opt_in_smem(reinterpret_cast<const void *>(kern), kSmemLimitLogits, done, ctx));
                 BwPipeParams pp{};
                 pp.f = a.f;
                 pp.dHout = a.dHout;
@@ -750,8 +743,8 @@ struct StepBw {
         cudaError_t e;
         if (a.f.mix_logits || a.f.read_logits) {
             auto pk = hc_param_bwd_kernel<N>;
-            e = cudaFuncSetAttribute(pk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)hist);
-            if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "param backward smem: %s", cudaGetErrorString(e));
+            static std::atomic<bool> done[64];
+            HC_BW_TRY(opt_in_smem(reinterpret_cast<const void *>(pk), (int)kHistMost, done, ctx));
             const int64_t tok_per_block = (pthreads / 32) * Group<N>::TPW;
             int64_t pgrid = (a.f.T + tok_per_block - 1) / tok_per_block;
             if (pgrid > (int64_t)ctx.sms * 16) pgrid = (int64_t)ctx.sms * 16;

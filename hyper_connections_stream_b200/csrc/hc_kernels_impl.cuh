@@ -151,16 +151,9 @@ template <int N, typename S, int KIND, int GW = pipe_group_warps(N)>
 hc_status launch_pipe(const StepParams &p, const PipeShape &sh, int smem, const LaunchCtx &ctx,
                       cudaStream_t st, const PipeReduce &rd = PipeReduce{}) {
     auto kern = hc_pipe_kernel<N, S, KIND, GW>;
-    static std::atomic<int> configured[64];  // largest dynamic smem opted in so far, per device
-    if (ctx.device < 0 || ctx.device >= 64)
-        return set_error(HC_ERR_UNSUPPORTED, "device ordinal %d >= 64", ctx.device);
-    if (smem > configured[ctx.device].load()) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess)
-            return set_error(HC_ERR_CUDA, "cudaFuncSetAttribute(%d B smem): %s", smem,
-                             cudaGetErrorString(e));
-        configured[ctx.device].store(smem);
-    }
+    static std::atomic<bool> done[64];
+    const hc_status opted = opt_in_smem(reinterpret_cast<const void *>(kern), kSmemLimit, done, ctx);
+    if (opted != HC_OK) return opted;
     int64_t grid = ctx.sms;
     if (grid > p.T) grid = p.T;
     kern<<<(unsigned)grid, pipe_threads_gw(GW, pipe_param_warps(N)), smem, st>>>(p, sh, ctx.fault, rd);

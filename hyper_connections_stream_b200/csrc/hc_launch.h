@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "hc_api.h"
 #include "hc_device.cuh"
 
@@ -21,6 +23,22 @@ struct LaunchCtx {
 
 // Record the calling thread's error text and return st.
 hc_status set_error(hc_status st, const char *fmt, ...);
+
+// Let `kern` be launched with up to `bytes` of dynamic shared memory on the
+// current device, once per device (done: one flag a device, of this kernel).
+// `bytes` is the most that any launch of it asks for, not this call's need: the
+// setting is the process's, and a call on another host thread that lowered it
+// between here and this call's launch would have the launch refused.
+inline hc_status opt_in_smem(const void *kern, int bytes, std::atomic<bool> (&done)[64], const LaunchCtx &ctx) {
+    if (ctx.device < 0 || ctx.device >= 64)
+        return set_error(HC_ERR_UNSUPPORTED, "device ordinal %d >= 64", ctx.device);
+    if (done[ctx.device].load(std::memory_order_acquire)) return HC_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess)
+        return set_error(HC_ERR_CUDA, "cudaFuncSetAttribute(%d B smem): %s", bytes, cudaGetErrorString(e));
+    done[ctx.device].store(true, std::memory_order_release);
+    return HC_OK;
+}
 
 // Launch one step kind (KIND_READ / KIND_WRITE / KIND_FUSED) for n streams.
 template <typename S, int KIND>

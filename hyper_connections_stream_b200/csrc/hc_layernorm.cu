@@ -880,11 +880,13 @@ struct LayerNorm {
         return (int)nt;
     }
     template <bool PACKED>
-    static hc_status occupancy(int64_t d, int &per_sm) {
+    static hc_status occupancy(int64_t d, const LaunchCtx &ctx, int &per_sm) {
         auto kern = hc_layernorm_bwd_kernel<N, S, PACKED>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 32768 * 4);
-        if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads(d), (size_t)d * 4);
+        static std::atomic<bool> done[64];
+        const hc_status s = opt_in_smem(reinterpret_cast<const void *>(kern), 32768 * 4, done, ctx);
+        if (s != HC_OK) return s;
+        const cudaError_t e =
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads(d), (size_t)d * 4);
         if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "layer norm occupancy: %s", cudaGetErrorString(e));
         return HC_OK;
     }
@@ -917,7 +919,7 @@ struct LayerNorm {
         int64_t smem = 0;
         int per_sm = 1;
         if (!ring(d, packed, smem).gw) {
-            const hc_status s = packed ? occupancy<true>(d, per_sm) : occupancy<false>(d, per_sm);
+            const hc_status s = packed ? occupancy<true>(d, ctx, per_sm) : occupancy<false>(d, ctx, per_sm);
             if (s != HC_OK) return s;
         }
         g = (int64_t)ctx.sms * (per_sm < 1 ? 1 : per_sm);
@@ -938,15 +940,9 @@ struct LayerNorm {
         cudaError_t e;
         if (sh.gw) {
             auto kern = hc_layernorm_bwd_ring_kernel<N, S, PACKED>;
-            static std::atomic<int> configured[64];  // largest opt-in so far, per device
-            if (ctx.device < 0 || ctx.device >= 64)
-                return set_error(HC_ERR_UNSUPPORTED, "device ordinal %d >= 64", ctx.device);
-            if (smem > configured[ctx.device].load()) {
-                e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-                if (e != cudaSuccess)
-                    return set_error(HC_ERR_CUDA, "layer norm smem attribute: %s", cudaGetErrorString(e));
-                configured[ctx.device].store((int)smem);
-            }
+            static std::atomic<bool> done[64];
+            const hc_status s = opt_in_smem(reinterpret_cast<const void *>(kern), kSmemLimitLogits, done, ctx);
+            if (s != HC_OK) return s;
             kern<<<(unsigned)g, 32 * (2 + sh.ng * sh.gw), (size_t)smem, st>>>(bp, sh, ctx.fault);
         } else {
             hc_layernorm_bwd_kernel<N, S, PACKED><<<(unsigned)g, threads(bp.f.d), (size_t)bp.f.d * 4, st>>>(bp);

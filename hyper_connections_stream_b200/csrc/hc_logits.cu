@@ -307,17 +307,9 @@ hc_status launch_mix_logits(const void *H, const void *W, float *z, int64_t T, i
     ms = make_tma_map_bf16(&mapW, W, (uint64_t)lp.K, (uint64_t)P, kLgKSub, (uint32_t)lp.Npad);
     if (ms != HC_OK) return ms;
 
-    static std::atomic<int> configured[64];  // largest dynamic smem opted in so far, per device
-    if (ctx.device < 0 || ctx.device >= 64)
-        return set_error(HC_ERR_UNSUPPORTED, "device ordinal %d >= 64", ctx.device);
-    if (smem > configured[ctx.device].load()) {
-        cudaError_t e = cudaFuncSetAttribute(hc_logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem);
-        if (e != cudaSuccess)
-            return set_error(HC_ERR_CUDA, "cudaFuncSetAttribute(%d B smem): %s", smem,
-                             cudaGetErrorString(e));
-        configured[ctx.device].store(smem);
-    }
+    static std::atomic<bool> done[64];
+    const hc_status opted = opt_in_smem(reinterpret_cast<const void *>(hc_logits_kernel), kSmemLimitLogits, done, ctx);
+    if (opted != HC_OK) return opted;
     const int64_t grid = (T + lp.rows - 1) / lp.rows;
     hc_logits_kernel<<<(unsigned)grid, kLgThreads, smem, st>>>(mapH, mapW, lp, ctx.fault);
     cudaError_t e = cudaGetLastError();
