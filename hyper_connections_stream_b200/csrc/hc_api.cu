@@ -641,7 +641,8 @@ hc_status hc_ipc_export(const void *dev_ptr, void *handle, uint64_t *offset) {
     if (!range_fn) return fail(HC_ERR_CUDA, "%s: cuMemGetAddressRange is not available", fn);
     CUdeviceptr base = 0;
     size_t bytes = 0;
-    const CUresult cr = range_fn(&base, &bytes, reinterpret_cast<CUdeviceptr>(dev_ptr));
+    const CUresult cr =
+        hc::with_context([&] { return range_fn(&base, &bytes, reinterpret_cast<CUdeviceptr>(dev_ptr)); });
     if (cr != CUDA_SUCCESS) return fail(HC_ERR_CUDA, "%s: cuMemGetAddressRange failed (%d)", fn, (int)cr);
     cudaIpcMemHandle_t h;
     const cudaError_t e = cudaIpcGetMemHandle(&h, reinterpret_cast<void *>(base));

@@ -24,6 +24,19 @@ struct LaunchCtx {
 // Record the calling thread's error text and return st.
 hc_status set_error(hc_status st, const char *fmt, ...);
 
+// The result of a driver call, made again with the current device's context
+// bound to this host thread if there was none (a thread may make its first call
+// here; runtime calls bind the context themselves, driver calls do not).
+template <typename Call>
+CUresult with_context(Call &&call) {
+    CUresult r = call();
+    if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = call();
+    }
+    return r;
+}
+
 // Let `kern` be launched with up to `bytes` of dynamic shared memory on the
 // current device, once per device (done: one flag a device, of this kernel).
 // `bytes` is the most that any launch of it asks for, not this call's need: the

@@ -9,6 +9,7 @@ next to nothing between them that holds the interpreter: the C calls overlap
 nearly all the time."""
 from __future__ import annotations
 
+import ctypes
 import os
 import subprocess
 import sys
@@ -179,3 +180,37 @@ def test_longer_and_longer_rows_in_a_fresh_process(hc, which):
     out = subprocess.run([sys.executable, "-c", _CHILD, which], capture_output=True, text=True, cwd=ROOT, timeout=300,
                          env=dict(os.environ, PYTHONPATH=ROOT))
     assert out.returncode == 0, (out.stdout[-2000:], out.stderr[-2000:])
+
+
+def test_first_call_of_a_host_thread(hc):
+    """Entry points that make a driver call (tensor maps; a buffer's range), from
+    threads that have made no CUDA call before."""
+    H, W, X, Wo = normal(37, 4, 64).to(BF), normal(24, 256).to(BF), normal(37, 64).to(BF), normal(64, 64).to(BF)
+    A, b = normal(4, 4), normal(4)
+    calls = [lambda: hc.mix_logits(H, W), lambda: hc.linear_then_write(X, Wo, H, A, b)]
+    want = [c() for c in calls]
+    s = torch.cuda.current_stream().cuda_stream
+    for call, ref in zip(calls, want):
+        fn, args, res = ready(hc, call)
+        got = []
+        t = threading.Thread(target=lambda: got.append((fn(*args, s), hc.lib().hc_last_error().decode())))
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert got == [(0, "")]
+        assert torch.equal(res, ref)
+    buf, got = normal(1 << 20), []
+    handle, offset = ctypes.create_string_buffer(64), ctypes.c_uint64(0)
+    t = threading.Thread(target=lambda: got.append(hc.lib().hc_ipc_export(buf.data_ptr(), handle, ctypes.byref(offset))))
+    t.start()
+    t.join()
+    assert got == [0]
+
+
+def test_mixing_logits_of_few_and_many_columns(hc):
+    """The tensor-core logits' stages go by P."""
+    def make(P):
+        H, W = normal(2, 4, 64).to(BF), normal(P, 256).to(BF)
+        return ready(hc, lambda: (hc.mix_logits(H, W), H, W))
+    rows = [make(P) for P in range(8, 129, 8)]
+    assert together(hc, [rows] * 4, 200) == []
