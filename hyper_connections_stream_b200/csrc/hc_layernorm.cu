@@ -11,8 +11,10 @@
 // Moments: every warp sums about its own mean, and the warps' sums are moved to
 // the token's mean (Chan's formula), so a mean much larger than the deviation
 // costs no accuracy and one exchange a token is enough; all in fp32, so a row
-// whose squares overflow fp32 has no finite norm. (The direct backward sums
-// about a pivot in each thread and adds in fp64; adding in fp64 in the forward
+// whose squares overflow fp32 has no finite norm. A warp's mean is rounded like
+// any fp32 sum of the raw values; its sum of h about itself is what that lost,
+// and goes along. (The direct backward sums about a pivot in each thread, moves
+// the sums to the row's first h and adds in fp64; adding in fp64 in the forward
 // cost a fifth of its time.)
 //
 // hc_layernorm_kernel keeps a token's h in registers between the statistic and
@@ -63,9 +65,14 @@ struct Moments {
         m2 += ms.x + ms.y;
         count += 2 * VP;
     }
-    __device__ __forceinline__ double sum() const { return (double)count * (double)p + (double)r; }
-    __device__ __forceinline__ double squares() const {
-        return (double)m2 + (double)p * (2.0 * (double)r + (double)count * (double)p);
+    // Sums of h - c and of its square. c is near the row's values, like p: about
+    // zero the squares would cancel when the mean is far (2^-53 of its square).
+    __device__ __forceinline__ double sum(float c) const {
+        return (double)count * ((double)p - (double)c) + (double)r;
+    }
+    __device__ __forceinline__ double squares(float c) const {
+        const double q = (double)p - (double)c;
+        return (double)m2 + q * (2.0 * (double)r + (double)count * q);
     }
 };
 
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
 hc_layernorm_bwd_kernel(LnBwParams bp) {
     const StepParams &p = bp.f;
     constexpr int V = StorageTraits<S>::V, VP = V / 2, NW = kBwdThreads / 32;
-    __shared__ float sa[kTB * N];
+    __shared__ float sa[kTB * N], sn[kTB];
     __shared__ double sums[2 * NW * 4];
     __shared__ float red[NW * N];
     __shared__ float swork[NW * kGroupScratch];
@@ -269,10 +276,23 @@ hc_layernorm_bwd_kernel(LnBwParams bp) {
         __syncthreads();  // previous batch's weights no longer read
         read_weights<N>(p, first, G, TB, sa, swork);
         __syncthreads();
+        // the first h of every row of the batch: what its threads' sums are moved to
+        if (tid < TB && first + (int64_t)tid * G < p.T) {
+            float near = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float2 v[VP];
+                load_row((first + (int64_t)tid * G) * N + i, 0, v);
+                near = __fmaf_rn(sa[tid * N + i], v[0].x, near);
+            }
+            sn[tid] = near;
+        }
+        __syncthreads();
         for (int tt = 0; tt < TB; ++tt) {
             const int64_t t = first + (int64_t)tt * G;
             if (t >= p.T) break;  // uniform over the CTA
             const float *at = sa + tt * N;
+            const float near = sn[tt];
             // ---- pass 1: moments of h, sums of u and u h ----
             Moments mo;
             float su = 0.0f, sud = 0.0f;  // sum u, sum u (h - p)
@@ -304,14 +324,15 @@ hc_layernorm_bwd_kernel(LnBwParams bp) {
                 for (int e = 0; e < VP; e += 2)
                     *reinterpret_cast<float4 *>(shp + k + 2 * e) = make_float4(h[e].x, h[e].y, h[e + 1].x, h[e + 1].y);
             }
-            double v[4] = {mo.sum(), mo.squares(), (double)su, (double)sud + (double)mo.p * (double)su};
+            double v[4] = {mo.sum(near), mo.squares(near), (double)su,
+                           (double)sud + ((double)mo.p - (double)near) * (double)su};
             cta_sums<4>(v, sums, parity, nwarps, lane, warp);
             parity ^= 1;
-            const double mu = v[0] / (double)d;
-            double var = v[1] / (double)d - mu * mu;
+            const double md = v[0] / (double)d, mu = (double)near + md;  // the mean less near, the mean
+            double var = v[1] / (double)d - md * md;
             var = var < 0.0 ? 0.0 : var;  // rounding only (NaN stays)
             const double rsd = 1.0 / sqrt(var + (double)p.eps);
-            const double c2d = rsd * (v[3] - mu * v[2]) / (double)d;  // mean(u z)
+            const double c2d = rsd * (v[3] - md * v[2]) / (double)d;  // mean(u z)
             const float muf = (float)mu, mul = (float)(mu - (double)muf), rs = (float)rsd;
             const float c1 = (float)(v[2] / (double)d), c2 = (float)c2d;
             const float2 nm = make_float2(-muf, -muf), nl = make_float2(-mul, -mul), r2 = make_float2(rs, rs);
@@ -400,8 +421,9 @@ hc_layernorm_bwd_kernel(LnBwParams bp) {
 //
 // A token takes one exchange: every warp sums about its own mean, and the
 // statistic warp moves the warps' sums to the token's mean (Chan's formula; all
-// terms are differences of means, so a mean far from zero costs no accuracy,
-// and no exchange is needed to find it first). While it does, the group runs
+// terms are differences of means and what the warp's mean lost to rounding, its
+// sum of h about itself, so a mean far from zero costs no accuracy, and no
+// exchange is needed to find it first). While it does, the group runs
 // the next token's first pass; the second pass of a token comes after that.
 //
 // Every wait is bounded (hc_sync.cuh); on time-out the fault code is recorded
@@ -416,9 +438,13 @@ struct LnRingShape {
     int stage_bytes;
 };
 
-// Floats of a group's exchange: two tokens' [4][32 warps] sums, [8] statistics,
-// [n][32 warps] da sums.
-__host__ __device__ constexpr int ln_red_floats(int n) { return 2 * (4 * 32 + 8 + n * 32); }
+// Floats of a group's exchange: two tokens' sums [kLnRows][32 warps], [8]
+// statistics, [n][32 warps] da sums. A warp's sums: of (h - m)^2, of u, of
+// u (h - m) and of h - m, with m its mean of h as rounded, then m itself. (Three
+// of the eight rows are not used: with five the second token's lie at no power
+// of two, and the addresses cost the kernel 4 %.)
+constexpr int kLnRows = 8;
+__host__ __device__ constexpr int ln_red_floats(int n) { return 2 * (kLnRows * 32 + 8 + n * 32); }
 __host__ __device__ inline int64_t ln_ring_fixed_bytes(int n, int64_t d, int ng, int nst) {
     return d * 4 + (int64_t)ng * ln_red_floats(n) * 4             // g, exchanges
            + (int64_t)(nst + 2 * ng + 2) * kMaxStreams * 4        // weights
@@ -434,7 +460,7 @@ __global__ void __launch_bounds__(32 * (kRingWarps + 2), 1)
 hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
     const StepParams &p = bp.f;
     constexpr int V = StorageTraits<S>::V, VP = V / 2;
-    constexpr int RF = ln_red_floats(N), kStat = 2 * 4 * 32, kDa = kStat + 2 * 8;
+    constexpr int RF = ln_red_floats(N), kStat = 2 * kLnRows * 32, kDa = kStat + 2 * 8;
     const int d = (int)p.d, ns = (int)bp.ns, nst = sh.nst, GW = sh.gw, NG = sh.ng;
     const int64_t G = gridDim.x;
     const int64_t M = (p.T > (int64_t)blockIdx.x) ? (p.T - 1 - blockIdx.x) / G + 1 : 0;
@@ -555,12 +581,13 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
         int g = 0, par = 0, wo = 0;  // wo: place of the weights of the next da
         uint32_t ph = 0;
         for (int64_t m = 0; m < M; ++m) {
-            float *rq = red + g * RF + par * 4 * 32, *so = red + g * RF + kStat + par * 8;
+            float *rq = red + g * RF + par * kLnRows * 32, *so = red + g * RF + kStat + par * 8;
             mbar_wait_bounded(&sums[g * 2 + par], ph, abort_flag, fault, FAULT_WAIT_REDUCE);
             // lane w: warp w's sums about its mean, moved to the mean of all
             const float q = rq[lane], u = rq[32 + lane], z = rq[64 + lane];
-            const float m0 = rq[96], dm = n_w > 0.0f ? rq[96 + lane] - m0 : 0.0f;
-            float mu = n_w * dm, su = u;
+            const float l = rq[96 + lane];
+            const float m0 = rq[128], dm = n_w > 0.0f ? rq[128 + lane] - m0 : 0.0f;
+            float mu = __fmaf_rn(n_w, dm, l), su = u;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 mu += __shfl_xor_sync(0xffffffffu, mu, o);
@@ -568,14 +595,14 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
             }
             mu *= inv_d;  // the mean less m0
             const float del = dm - mu;
-            float sq = __fmaf_rn(n_w * del, del, q), sz = __fmaf_rn(del, u, z);
+            float sq = __fmaf_rn(del, __fmaf_rn(n_w, del, 2.0f * l), q), sz = __fmaf_rn(del, u, z);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 sq += __shfl_xor_sync(0xffffffffu, sq, o);
                 sz += __shfl_xor_sync(0xffffffffu, sz, o);
             }
             // dh = rs (u - c1 - c2 z), z = (h - mean) rs
-            const float rs = __frsqrt_rn(__fmaf_rn(sq, inv_d, p.eps));  // sq >= 0
+            const float rs = __frsqrt_rn(__fmaf_rn(sq < 0.0f ? 0.0f : sq, inv_d, p.eps));  // below 0: rounding only
             const float c1 = su * inv_d, c2 = rs * sz * inv_d;
             if (bp.da && m >= 2 * NG) {
                 write_da(m - 2 * NG, g, par, wo);
@@ -679,9 +706,9 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) wm1 += __shfl_xor_sync(0xffffffffu, wm1, o);
             wm1 *= inv_n;
-            float2 q[3];
+            float2 q[4];
 #pragma unroll
-            for (int x = 0; x < 3; ++x) q[x] = make_float2(0.0f, 0.0f);
+            for (int x = 0; x < 4; ++x) q[x] = make_float2(0.0f, 0.0f);
             const float2 nm = make_float2(-wm1, -wm1);
 #pragma unroll
             for (int u = 0; u < kCPT; ++u) {
@@ -697,13 +724,14 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
                         q[0] = ffma2_rn(h1[u][e], h1[u][e], q[0]);
                         q[1] = fadd2_rn(q[1], w);
                         q[2] = ffma2_rn(w, h1[u][e], q[2]);
+                        q[3] = fadd2_rn(q[3], h1[u][e]);
                     }
                 }
             }
-            const float v[3] = {q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y};
-            float *rq = rg + (int)(i & 1) * 4 * 32 + gw;
-            warp_sums_put<3>(v, lane, [&](int x, float sx) { rq[x * 32] = sx; });
-            if (lane == 0) rq[3 * 32] = wm1;
+            const float v[4] = {q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y, q[3].x + q[3].y};
+            float *rq = rg + (int)(i & 1) * kLnRows * 32 + gw;
+            warp_sums_put<4>(v, lane, [&](int x, float sx) { rq[x * 32] = sx; });
+            if (lane == 0) rq[4 * 32] = wm1;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sums[g * 2 + (int)(i & 1)]);
             for (slot += NG; slot >= nst; slot -= nst) ph ^= 1u;
