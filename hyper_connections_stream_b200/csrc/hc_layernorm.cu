@@ -10,8 +10,9 @@
 //
 // Moments: every warp sums about its own mean, and the warps' sums are moved to
 // the token's mean (Chan's formula), so a mean much larger than the deviation
-// costs no accuracy and one exchange a token is enough; all in fp32, so a row
-// whose squares overflow fp32 has no finite norm. A warp's mean is rounded like
+// costs no accuracy and one exchange a token is enough; all in fp32, and the sum
+// of squares leaves a thread divided by d, so that a row is NaN only where a
+// thread's own overflow (inv_norm). A warp's mean is rounded like
 // any fp32 sum of the raw values; its sum of h about itself is what that lost,
 // and goes along. (The direct backward sums about a pivot in each thread, moves
 // the sums to the row's first h and adds in fp64; adding in fp64 in the forward
@@ -110,11 +111,11 @@ __device__ __forceinline__ void read_weights(const StepParams &p, int64_t first,
 
 template <int N, typename S, int CPT>
 __global__ void __launch_bounds__(kFwdThreads)
-hc_layernorm_kernel(StepParams p, const float *beta) {
+hc_layernorm_kernel(StepParams p, const float *beta, float inv_d) {
     constexpr int V = StorageTraits<S>::V, VP = V / 2;
     __shared__ float sa[kTB * N];
     // of alternate tokens: the warps' means, and their sums of squares and of h
-    // about them (the latter is what the mean's rounding left)
+    // about them (the latter is what the mean's rounding left), over d
     __shared__ float sums[2][3][32];
     __shared__ float swork[kFwdThreads / 32 * kGroupScratch];
     const int tid = threadIdx.x, NT = blockDim.x, nwarps = NT >> 5;
@@ -130,8 +131,7 @@ hc_layernorm_kernel(StepParams p, const float *beta) {
         return (float)n;
     };
     const float n_own = warp_columns(warp), inv_n = n_own > 0.0f ? 1.0f / n_own : 0.0f;
-    const float n_w = lane < nwarps ? warp_columns(lane) : 0.0f;  // lane w: warp w
-    const float inv_d = 1.0f / (float)d;
+    const float f_w = lane < nwarps ? warp_columns(lane) * inv_d : 0.0f;  // lane w: warp w's part of the row
     int TB = nwarps * Group<N>::TPW;
     TB = TB < kTB ? TB : kTB;
     const S *H = static_cast<const S *>(p.H);
@@ -187,24 +187,23 @@ hc_layernorm_kernel(StepParams p, const float *beta) {
                     }
                 }
             }
-            const float v[2] = {q2.x + q2.y, l2.x + l2.y};
+            const float v[2] = {(q2.x + q2.y) * inv_d, (l2.x + l2.y) * inv_d};
             warp_sums_put<2>(v, lane, [&](int x, float sx) { sums[parity][1 + x][warp] = sx; });
             if (lane == 0) sums[parity][0][warp] = wm;
             __syncthreads();
             // moved to the mean of all: lane w takes warp w's
-            const bool has = n_w > 0.0f;
+            const bool has = f_w > 0.0f;
             const float m0 = sums[parity][0][0], dm = has ? sums[parity][0][lane] - m0 : 0.0f;
             const float sl = has ? sums[parity][2][lane] : 0.0f, s2 = has ? sums[parity][1][lane] : 0.0f;
             parity ^= 1;
-            float mu = __fmaf_rn(n_w, dm, sl);
+            float mu = __fmaf_rn(f_w, dm, sl);  // the mean less m0
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mu += __shfl_xor_sync(0xffffffffu, mu, o);
-            mu *= inv_d;  // the mean less m0
             const float del = dm - mu;
-            float sq = __fmaf_rn(del, __fmaf_rn(n_w, del, 2.0f * sl), s2);
+            float sq = __fmaf_rn(del, __fmaf_rn(f_w, del, 2.0f * sl), s2);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            const float rs = __frsqrt_rn(__fmaf_rn(sq < 0.0f ? 0.0f : sq, inv_d, p.eps));  // below 0: rounding only
+            const float rs = inv_norm(sq < 0.0f ? 0.0f : sq, p.eps);  // below 0: rounding only
             const float own = (wm - m0) - mu;  // the warp's mean less the token's
             const float2 nz = make_float2(own, own), r2 = make_float2(rs, rs);
 #pragma unroll
@@ -330,7 +329,7 @@ hc_layernorm_bwd_kernel(LnBwParams bp) {
             parity ^= 1;
             const double md = v[0] / (double)d, mu = (double)near + md;  // the mean less near, the mean
             double var = v[1] / (double)d - md * md;
-            var = var < 0.0 ? 0.0 : var;  // rounding only (NaN stays)
+            var = var < 0.0 ? 0.0 : var < INFINITY ? var : NAN;  // below 0: rounding only
             const double rsd = 1.0 / sqrt(var + (double)p.eps);
             const double c2d = rsd * (v[3] - md * v[2]) / (double)d;  // mean(u z)
             const float muf = (float)mu, mul = (float)(mu - (double)muf), rs = (float)rsd;
@@ -439,10 +438,10 @@ struct LnRingShape {
 };
 
 // Floats of a group's exchange: two tokens' sums [kLnRows][32 warps], [8]
-// statistics, [n][32 warps] da sums. A warp's sums: of (h - m)^2, of u, of
-// u (h - m) and of h - m, with m its mean of h as rounded, then m itself. (Three
-// of the eight rows are not used: with five the second token's lie at no power
-// of two, and the addresses cost the kernel 4 %.)
+// statistics, [n][32 warps] da sums. A warp's sums: of (h - m)^2, over d, of u,
+// of u (h - m) and of h - m, with m its mean of h as rounded, then m itself.
+// (Three of the eight rows are not used: with five the second token's lie at no
+// power of two, and the addresses cost the kernel 4 %.)
 constexpr int kLnRows = 8;
 __host__ __device__ constexpr int ln_red_floats(int n) { return 2 * (kLnRows * 32 + 8 + n * 32); }
 __host__ __device__ inline int64_t ln_ring_fixed_bytes(int n, int64_t d, int ng, int nst) {
@@ -563,7 +562,7 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
 
     if (warp == NG * GW + 1) {
         // ---------------- statistics ----------------
-        const float n_w = lane < GW ? (float)warp_columns(lane) : 0.0f;  // lane w: warp w of the group
+        const float f_w = lane < GW ? (float)warp_columns(lane) * inv_d : 0.0f;  // lane w: warp w's part of the row
         // da of the CTA's token m (of group gg), whose sums are in buffer par
         auto write_da = [&](int64_t m, int gg, int par, int place) {
             const float *dr = red + gg * RF + kDa + par * N * 32;
@@ -584,26 +583,25 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
             float *rq = red + g * RF + par * kLnRows * 32, *so = red + g * RF + kStat + par * 8;
             mbar_wait_bounded(&sums[g * 2 + par], ph, abort_flag, fault, FAULT_WAIT_REDUCE);
             // lane w: warp w's sums about its mean, moved to the mean of all
-            const float q = rq[lane], u = rq[32 + lane], z = rq[64 + lane];
-            const float l = rq[96 + lane];
-            const float m0 = rq[128], dm = n_w > 0.0f ? rq[128 + lane] - m0 : 0.0f;
-            float mu = __fmaf_rn(n_w, dm, l), su = u;
+            const float q = rq[lane], u = rq[32 + lane] * inv_d, z = rq[64 + lane] * inv_d;
+            const float l = rq[96 + lane] * inv_d;
+            const float m0 = rq[128], dm = f_w > 0.0f ? rq[128 + lane] - m0 : 0.0f;
+            float mu = __fmaf_rn(f_w, dm, l), su = u;  // the mean less m0, mean u
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 mu += __shfl_xor_sync(0xffffffffu, mu, o);
                 su += __shfl_xor_sync(0xffffffffu, su, o);
             }
-            mu *= inv_d;  // the mean less m0
             const float del = dm - mu;
-            float sq = __fmaf_rn(del, __fmaf_rn(n_w, del, 2.0f * l), q), sz = __fmaf_rn(del, u, z);
+            float sq = __fmaf_rn(del, __fmaf_rn(f_w, del, 2.0f * l), q), sz = __fmaf_rn(del, u, z);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 sq += __shfl_xor_sync(0xffffffffu, sq, o);
                 sz += __shfl_xor_sync(0xffffffffu, sz, o);
             }
             // dh = rs (u - c1 - c2 z), z = (h - mean) rs
-            const float rs = __frsqrt_rn(__fmaf_rn(sq < 0.0f ? 0.0f : sq, inv_d, p.eps));  // below 0: rounding only
-            const float c1 = su * inv_d, c2 = rs * sz * inv_d;
+            const float rs = inv_norm(sq < 0.0f ? 0.0f : sq, p.eps);  // below 0: rounding only
+            const float c1 = su, c2 = rs * sz;
             if (bp.da && m >= 2 * NG) {
                 write_da(m - 2 * NG, g, par, wo);
                 if (++wo == sh.nw) wo = 0;
@@ -728,7 +726,7 @@ hc_layernorm_bwd_ring_kernel(LnBwParams bp, LnRingShape sh, int *fault) {
                     }
                 }
             }
-            const float v[4] = {q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y, q[3].x + q[3].y};
+            const float v[4] = {(q[0].x + q[0].y) * inv_d, q[1].x + q[1].y, q[2].x + q[2].y, q[3].x + q[3].y};
             float *rq = rg + (int)(i & 1) * kLnRows * 32 + gw;
             warp_sums_put<4>(v, lane, [&](int x, float sx) { rq[x * 32] = sx; });
             if (lane == 0) rq[4 * 32] = wm1;
@@ -871,7 +869,7 @@ struct LayerNorm {
             const int64_t most = (int64_t)ctx.sms * (per_sm < 1 ? 1 : per_sm);
             if (grid > most) grid = most;
         }
-        kern<<<(unsigned)grid, NT, 0, st>>>(a.f, a.beta);
+        kern<<<(unsigned)grid, NT, 0, st>>>(a.f, a.beta, 1.0f / (float)a.f.d);
         e = cudaGetLastError();
         if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "hc_layernorm_kernel launch: %s", cudaGetErrorString(e));
         return HC_OK;

@@ -378,8 +378,10 @@ HC_API size_t hc_write_then_read_backward_checkpoint_workspace_bytes(hc_dtype dt
  *   beta: [d] fp32 or NULL for none, 16-byte aligned.
  *   a may be NULL when n == 1: weight 1, the plain layer norm of rows [T][d].
  * Other arguments as hc_read_rmsnorm. h and the moments in fp32 (sums about
- * means, so a mean far from zero costs nothing; squares that overflow fp32,
- * |h| above about 1e19, have no finite norm), x rounded once.
+ * means, so a mean far from zero costs nothing), x rounded once. A row that
+ * deviates from its mean by more than about 1e18, whose squares overflow fp32,
+ * is NaN; with eps = 0 one that deviates by less than about 1e-17 loses
+ * accuracy as its squares underflow.
  */
 HC_API hc_status hc_read_layernorm(const void *H, void *x, hc_dtype dt, int64_t T, int n, int64_t d,
                                    hc_read_mode rm, const float *a, int64_t a_tok_stride, const float *g,
