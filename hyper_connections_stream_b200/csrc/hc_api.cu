@@ -916,7 +916,8 @@ hc_status hc_write_then_read_backward_checkpoint(
     HC_TRY(check_stride(fn, "a_tok_stride", a_tok_stride));
     HC_TRY(check_eps(fn, eps));
     if (T == 0) {  // nothing to sum: the gain's gradient is zero
-        if (dg && aligned(dg, 4)) {
+        if (dg) {
+            if (!aligned(dg, 4)) return fail(HC_ERR_MISALIGNED, "%s: dg is not 4-byte aligned", fn);
             const cudaError_t e = cudaMemsetAsync(dg, 0, (size_t)d * 4, static_cast<cudaStream_t>(stream));
             if (e != cudaSuccess) return fail(HC_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
         }
@@ -1030,8 +1031,10 @@ hc_status hc_read_layernorm_backward(const void *H, const uint8_t *H_scales, hc_
     HC_TRY(check_eps(fn, eps));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) {  // nothing to sum: the gradients of g and beta are zero
+        if ((dg && !aligned(dg, 4)) || (dbeta && !aligned(dbeta, 4)))
+            return fail(HC_ERR_MISALIGNED, "%s: dg or dbeta is not 4-byte aligned", fn);
         for (float *o : {dg, dbeta}) {
-            if (!o || !aligned(o, 4)) continue;
+            if (!o) continue;
             const cudaError_t e = cudaMemsetAsync(o, 0, (size_t)d * 4, st);
             if (e != cudaSuccess) return fail(HC_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
         }
