@@ -125,7 +125,10 @@ bool pipe_shape(const StepParams &p, PipeShape &sh, int &smem) {
 // kinds, whose consumers then run on fewer registers, at n <= 2 (n = 2,
 // T = 16384: 71.7 -> 78.1 % of copy) and at n = 3, 4 only for calls of up to
 // 8192 tokens (n = 4: T = 1024 +5 %, T = 4096 +3 %, but T = 16384 -1 %).
-// Where seven-warp tiles fit exactly (d = 7168) the default stays.
+// Where seven-warp tiles fit exactly (d = 7168) the default stays. The saving
+// step takes the wider group at any token count (T = 12000, per-token Sinkhorn:
+// n = 3, d = 4096 258 -> 224 us; n = 4, d = 2048 200 -> 165, d = 4096 302 -> 273,
+// d = 6144 399 -> 394, only d = 8192 the other way, 494 -> 514).
 template <int N, int KIND>
 constexpr int pipe_alt_group_warps() { return N <= 4 ? 8 : pipe_group_warps(N); }
 
@@ -141,7 +144,7 @@ bool pipe_take_alt(int64_t d, int64_t T) {
     if constexpr (pipe_alt_group_warps<N, KIND>() == pipe_group_warps(N)) {
         return false;
     } else {
-        if (!(KIND == KIND_READ || KIND == KIND_WRITE) && N > 2 && T > 8192) return false;
+        if (!(KIND == KIND_READ || KIND == KIND_WRITE || KIND == KIND_SAVE) && N > 2 && T > 8192) return false;
         return pipe_padded_slices<N, S>(d, pipe_alt_group_warps<N, KIND>()) <
                pipe_padded_slices<N, S>(d, pipe_group_warps(N));
     }
@@ -182,7 +185,34 @@ int step_path_n(const StepParams &p, const LaunchCtx &ctx, bool &pipe_ok, bool &
     bool small = p.T * (int64_t)N * p.d * (int64_t)sizeof(S) * 2 < (int64_t(64) << 20);
     if constexpr (KIND == KIND_READ) small = true;
     if constexpr (KIND == KIND_WRITE && N <= 2) small = true;
-    if constexpr (KIND == KIND_FUSED || KIND == KIND_SAVE) {
+    if constexpr (KIND == KIND_SAVE) {
+        // The saving step stores the codes too, which its two families pay for
+        // differently, so the fused step's thresholds do not fit it. Both were
+        // timed at 612 points (n = 1 .. 8, d = 1024 .. 8192, T = 128 .. 16384,
+        // both types, matrix and Sinkhorn): this rule is 0.6 % behind the better
+        // side on average, the fused step's 3.6 %, with losses to 1.67. Up to
+        // four streams it goes by the bytes a token reads: pipelined against
+        // register-streaming in us, bf16, T = 8192 .. 16384: n = 1, d = 4096
+        // 191 : 172 (16 KB), d = 5120 175 : 260; n = 2, d = 4096 231 : 311; n = 3,
+        // d = 1024 132 : 81; n = 4, d = 4096 186 : 236. n = 5: by what the last
+        // tile leaves idle (d = 2048 363 : 283, 4096 541 : 554, 7168 809 : 974).
+        // Beyond, the codes' registers leave the pipeline too few warps: n = 6
+        // 1313 : 1155, n = 8 924 : 809; fp32 has half the codes a vector (n = 6,
+        // d = 7168 803 : 920).
+        const int64_t bytes = (N + 1) * p.d * (int64_t)sizeof(S);
+        const int64_t nvec = p.d / pipe_vec_elems<N, S>();
+        const int64_t slots = alt ? pipe_padded_slices<N, S>(p.d, GWA)
+                                  : pipe_padded_slices<N, S>(p.d, pipe_group_warps(N));
+        const int64_t idle = slots - nvec;
+        if constexpr (N <= 4) {
+            small = bytes < 20480 || p.T < (N <= 2 || bytes < 32768 ? 512 : 256);
+        } else if constexpr (N == 5) {
+            small = idle * 8 > slots || bytes < 30720 || p.T < (idle * 12 > slots ? 4096 : 512);
+        } else {
+            small = !(N == 6 && sizeof(S) == 4 && idle * 4 <= slots && p.T >= 2048);
+        }
+    }
+    if constexpr (KIND == KIND_FUSED) {
         constexpr int64_t tmin_n[9] = {0, 512, 512, 256, 256, 1024, 4096, 2048, 2048};
         constexpr int64_t ragged_x[9] = {0, int64_t(1) << 40, 64, 4, 4, 16, 4, 4, 4};
         // raggedness of the default width, which the thresholds were fitted on
