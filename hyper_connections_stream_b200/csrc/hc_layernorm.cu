@@ -916,6 +916,16 @@ struct LayerNorm {
         if (e != cudaSuccess) return set_error(HC_ERR_CUDA, "layer norm occupancy: %s", cudaGetErrorString(e));
         return HC_OK;
     }
+    // The ring takes rows from here up, in slices of 16 bytes of dx: below, a
+    // group of one or two warps pays a token's exchange for too few columns.
+    // Direct : ring in us, 134 MB of values a call, n = 1, 4 and 8: bf16 64
+    // slices 354 : 647, 199 : 326, 164 : 229 (268 MB); 96 217 : 233, 120 : 128,
+    // 97 : 96; 112 232 : 204, 124 : 114, 99 : 85; 128 220 : 183, 118 : 103,
+    // 93 : 81; 256 223 : 108, 120 : 69, 93 : 71. fp32, half the columns a slice:
+    // 112 171 : 200, 101 : 112, 83 : 81; 128 155 : 177, 93 : 99, 79 : 75; 130
+    // 203 : 177, 110 : 97, 89 : 75; 256 162 : 103, 97 : 65, 77 : 60. From a
+    // checkpoint alike (fp32 at n = 8 crosses at 96 already).
+    static constexpr int64_t kRingFrom = V == 8 ? 112 : 130;
     // The ring's geometry, or gw = 0 where it does not apply: a group's warps
     // must cover the row, two stages a group and one more
     // must fit (a group holds the tokens of both passes), and a checkpoint's
@@ -923,7 +933,7 @@ struct LayerNorm {
     static LnRingShape ring(int64_t d, bool packed, int64_t &smem) {
         LnRingShape sh{};
         const int64_t nvec = d / V, gw = (nvec + 32 * kCPT - 1) / (32 * kCPT);
-        if (gw > kRingWarps || (packed && d % 16 != 0)) return sh;
+        if (nvec < kRingFrom || gw > kRingWarps || (packed && d % 16 != 0)) return sh;
         const int64_t stage = N * (packed ? d + ck_scale_stride(d) : d * (int64_t)sizeof(S)) + d * (int64_t)sizeof(S);
         for (int64_t ng = kRingWarps / gw; ng >= 1; --ng) {
             int64_t nst = (kSmemLimitLogits - ln_ring_fixed_bytes(N, d, (int)ng, 0)) / (stage + kMaxStreams * 4 + 16);
@@ -940,7 +950,7 @@ struct LayerNorm {
         }
         return sh;
     }
-    // The grid, which the workspace is sized by: the larger of the two forms'.
+    // The grid, which the workspace is sized by (for the larger of the two forms').
     static hc_status grid(int64_t T, int64_t d, bool packed, const LaunchCtx &ctx, int64_t &g) {
         int64_t smem = 0;
         int per_sm = 1;
