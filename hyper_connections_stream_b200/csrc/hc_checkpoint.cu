@@ -3,14 +3,15 @@
 // the format).
 //
 // Both are bound by memory: a value costs its own bytes and 1 + 1/32. Measured
-// for T = 16384, n = 4, d = 7168, bf16 (1.42 GB each way): packing 242 us, 92 %
-// of the copy rate by DRAM counters' bytes; unpacking, which writes twice what
-// it reads, 309 us under the profiler, 72 %, and about 270 us in the pair. Two or
+// for T = 16384, n = 4, d = 7168, bf16 (1.42 GB each way): the pair 512 us, 85 %
+// of the copy rate; packing 242 us of it, 92 %; unpacking, which writes twice
+// what it reads, 309 us under the profiler, 72 %, and about 270 us in the pair. Two or
 // eight chunks in flight a thread, plain instead of streaming stores, and eight
 // times the CTAs were 1 to 18 % slower. A warp
-// takes one 256-element chunk of a row at a time, 16 bytes of codes' worth a
-// lane, so the 4 (bf16) or 8 (fp32) lanes of a block of 32 are neighbours and
-// the maximum is a shuffle or three; rows of any length end inside a chunk.
+// takes one chunk of a row at a time, 16 bytes of X a lane (256 elements in
+// bf16, 128 in fp32; 8 or 4 codes a lane), so the 4 or 8 lanes of a block of 32
+// are neighbours and the maximum is two or three shuffles; rows of any length
+// end inside a chunk.
 // Every thread has kUnroll chunks' loads in flight. The chunk's place is carried along
 // (row, chunk) instead of divided out.
 #include "hc_checkpoint.cuh"
@@ -115,8 +116,8 @@ hc_checkpoint_unpack_kernel(const uint8_t *Q, const uint8_t *E, S *X, int64_t ro
     }
 }
 
-// CTAs: enough for every chunk once, at most eight a multiprocessor (full
-// occupancy at 256 threads).
+// CTAs: enough for every chunk once, at most eight a multiprocessor (four are
+// resident at unpacking's 58 registers; fewer or more CTAs were not faster).
 int64_t grid_for(int64_t rows, int per_row, const LaunchCtx &ctx) {
     const int64_t chunks = rows * per_row, per_cta = kThreads / 32;
     int64_t grid = (chunks + per_cta - 1) / per_cta;

@@ -7,7 +7,8 @@
 // exact, so the only rounding is the code's own (half a step: 2^-4 of the
 // value while it stays above 2^-14 of the block's scale range), no value
 // saturates, and the kept value code * 2^e is exact in bf16 as well as in
-// fp32. The exponent is stored biased by 127 in one byte (E8M0), 1 .. 247.
+// fp32 (all but one: values from 1.9375 * 2^127 up round to 2^128, which both
+// types hold as infinity). The exponent is stored biased by 127 in one byte (E8M0), 1 .. 247.
 // A value that is not finite is kept as NaN and leaves its block's scale alone.
 //
 // Rows: codes [rows][d]; exponents [rows][ck_scale_stride(d)], the rows padded

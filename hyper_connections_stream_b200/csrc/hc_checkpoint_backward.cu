@@ -24,10 +24,10 @@
 // CTA's workspace row. All sums are fp32: a row whose squares overflow it has no
 // norm, and NaN gradients (hc_checkpoint_ring.cuh).
 //
-// Measured: n = 8, T = 2048, d = 4096, bf16 in 179 us with the parameter kernels;
-// n = 4, T = 16384, d = 7168 in 894 us, which the ring does in 708 (64 % of the
-// copy rate). The direct kernel is
-// held by latency: 14 warps of 128 registers on a multiprocessor at n = 4, 39 %
+// Measured: n = 8, T = 2048, d = 4096, bf16 in 181 us with the parameter kernels
+// (152 us of its own under the profiler, 42 % of the issue slots at eight warps
+// of 255 registers); n = 4, T = 16384, d = 7168 in 894 us, which the ring does in
+// 695 (65 % of the copy rate). At n = 4 the direct kernel is held by latency: 14 warps of 128 registers on a multiprocessor at n = 4, 39 %
 // of the issue slots and of the FMA pipes used, 99 instructions a column. What
 // did not help there: staging slices with cp.async (930 to 995), dH' and dx kept
 // in shared memory for the second pass (909), slices of half the width at 80

@@ -15,8 +15,8 @@
 // n < 3, and the gain gradient in registers. The two statistics of a token are
 // exchanged first; the other sums follow behind that wait.
 //
-// Measured: n = 4, T = 16384, d = 7168, bf16, Sinkhorn in 708 us with the
-// parameter kernels (64 % of the copy rate); bound by latency, half the issue
+// Measured: n = 4, T = 16384, d = 7168, bf16, Sinkhorn in 695 us with the
+// parameter kernels (65 % of the copy rate); bound by latency, half the issue
 // slots used. Fourteen warps of 128 registers spilled and took 813 us where this
 // split took 733 (timed in turn, before the groups of warps became one).
 //

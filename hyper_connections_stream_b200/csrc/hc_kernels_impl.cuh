@@ -196,9 +196,10 @@ int step_path_n(const StepParams &p, const LaunchCtx &ctx, bool &pipe_ok, bool &
         // 191 : 172 (16 KB), d = 5120 175 : 260; n = 2, d = 4096 231 : 311; n = 3,
         // d = 1024 132 : 81; n = 4, d = 4096 186 : 236. n = 5: by what the last
         // tile leaves idle (d = 2048 363 : 283, 4096 541 : 554, 7168 809 : 974).
-        // Beyond, the codes' registers leave the pipeline too few warps: n = 6
-        // 1313 : 1155, n = 8 924 : 809; fp32 has half the codes a vector (n = 6,
-        // d = 7168 803 : 920).
+        // Beyond, register-streaming (n = 6, d = 7168 1313 : 1155; n = 8, d = 4096
+        // 924 : 809; but d = 5120 845 : 949), although it spills there (n = 8: 24
+        // to 368 bytes a thread by slices); fp32 at n = 6 keeps the pipeline from
+        // 2048 tokens on (d = 7168 803 : 920).
         const int64_t bytes = (N + 1) * p.d * (int64_t)sizeof(S);
         const int64_t nvec = p.d / pipe_vec_elems<N, S>();
         const int64_t slots = alt ? pipe_padded_slices<N, S>(p.d, GWA)

@@ -19,17 +19,21 @@
 // cost a fifth of its time.)
 //
 // hc_layernorm_kernel keeps a token's h in registers between the statistic and
-// the store, so H is read once: T = 16384, n = 4, d = 4096, bf16 in 124 us, 83 %
+// the store, so H is read once: T = 16384, n = 4, d = 4096, bf16 in 126 us, 82 %
 // of the copy rate. hc_layernorm_bwd_ring_kernel, below, takes the rows that
-// its warps cover (d to 7168 bf16, 3584 fp32) and whose tokens fit its stages:
-// n = 1, T = 16384, d = 7168, bf16 in 193 us (56 % of the copy rate); n = 4 from
-// a checkpoint, T = 8192, in 205 us (62 %). It is held by its instructions'
-// latency: 14 warps with 128 registers a thread, half the issue slots used, the
-// shared memory's latency and the one exchange a token. More warps with fewer
-// registers spilled (335 us), two tokens at a time in one thread too (293 us).
-// hc_layernorm_bwd_kernel takes the rest: it parks h in shared memory (fp32),
+// its warps cover (d from 896 to 7168 in bf16, from 520 to 3584 in fp32) and of
+// which three whole tokens fit in shared memory: n = 1, T = 16384, d = 7168,
+// bf16 in 198 us (55 % of the copy rate); n = 4 from a checkpoint, T = 8192, in
+// 206 us (62 %). It is held by its instructions' latency: 14 warps with 128
+// registers a thread, half the issue slots used, the shared memory's latency and
+// the one exchange a token. More warps with fewer registers spilled (335 us),
+// two tokens at a time in one thread too (293 us).
+// hc_layernorm_bwd_kernel takes the rest, n = 4 at d = 7168 and n = 8 at d = 4096
+// in full precision and wider rows among it: it parks h in shared memory (fp32),
 // reads dx, and H for da, again from L2, and accumulates the gradients of g and
-// beta in the CTA's workspace row (522 us for the first of these cases).
+// beta in the CTA's workspace row (522 us for the first of these cases; n = 4,
+// T = 8192, d = 7168 398 us, 41 % of the copy rate; n = 1, T = 16384, d = 8192 591
+// us, 21 %).
 // Either leaves one row of partial sums a CTA, which are summed in a fixed
 // order.
 #include <atomic>

@@ -316,7 +316,9 @@ HC_API hc_status hc_write_then_read_backward_noalloc(
  *   max|x| / 2^e <= 448 over the block's finite values, at least -126; a value
  *   is kept as the e4m3 code of x / 2^e (round to nearest even; nothing
  *   saturates). The kept value, code * 2^e, is exact in bf16 and fp32 except
- *   below the type's smallest normal. A value that is not finite is kept as
+ *   below the type's smallest normal, and except that a value from 1.9375 *
+ *   2^127 up (the last thirtieth of the range) rounds to 2^128: it unpacks as
+ *   infinity, and the gradients taken from it are NaN. A value that is not finite is kept as
  *   NaN and does not move its block's scale; a block of zeros has e = -126.
  *   codes  [rows][d], one byte a value (e4m3);
  *   scales [rows][hc_checkpoint_scale_stride(d)], e + 127 in one byte a block,

@@ -12,6 +12,15 @@ here). Checkpoint, C = 192: as in test_gpu_checkpoint_range.py, n + 1 at most 9
 and one add a token; Sinkhorn adds 2 K (n + 1) and the softmax 2 n + 8, and
 gradients of logits have the bar of the full-precision backward's tests, 2e-4
 of the largest.
+
+The chains of fp32 roundings as the kernels have them, which the bars of 64 and
+32 of the other training tests stand for as well. Backward from a checkpoint:
+h n + 1; a thread's sum 24 (three slices of 8 in turn) or 5 and an add a slice
+(16 at the widest); 1 for the division by d; 5 exchanges; 6 or 8 for the warps:
+at most 36 and 44 with h. Layer norm: a thread's squares 32 (8 slices), 5
+exchanges, 5 for the warps, of which the inverse norm takes half; the mean's
+own rounding is carried along and costs nothing. dg and dbeta: one add a token
+of a CTA before the rows of partial sums are added in fp64.
 """
 from __future__ import annotations
 

@@ -70,8 +70,8 @@ def test_pipelined(hc, n, slices, dt, logits):
 
 @pytest.mark.parametrize("T,n,d,dt", [(4096, 4, 4096, "bf16"), (9000, 3, 4096, "bf16"), (1300, 3, 2048, "f32")])
 def test_eight_warp_groups_where_the_rule_takes_them(hc, T, n, d, dt):
-    """The static layer's size, and either side of the 8192 tokens that bound
-    the eight-warp groups beyond two streams."""
+    """The static layer's size, and sizes on either side of the 8192 tokens that
+    bound the fused step's eight-warp groups (not this step's)."""
     for path in (hc.PATH_AUTO, hc.PATH_PIPELINED):
         _check(hc, path, T, n, d, dt, False)
 
