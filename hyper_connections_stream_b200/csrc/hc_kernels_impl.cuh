@@ -206,9 +206,9 @@ int step_path_n(const StepParams &p, const LaunchCtx &ctx, bool &pipe_ok, bool &
                                   : pipe_padded_slices<N, S>(p.d, pipe_group_warps(N));
         const int64_t idle = slots - nvec;
         if constexpr (N <= 4) {
-            small = bytes < 20480 || p.T < (N <= 2 || bytes < 32768 ? 512 : 256);
+            small = bytes < (20 << 10) || p.T < (N <= 2 || bytes < (32 << 10) ? 512 : 256);
         } else if constexpr (N == 5) {
-            small = idle * 8 > slots || bytes < 30720 || p.T < (idle * 12 > slots ? 4096 : 512);
+            small = idle * 8 > slots || bytes < (30 << 10) || p.T < (idle * 12 > slots ? 4096 : 512);
         } else {
             small = !(N == 6 && sizeof(S) == 4 && idle * 4 <= slots && p.T >= 2048);
         }
